@@ -217,12 +217,12 @@ def _packed_plain(s):
 
 def _prefix_own(s):
     import gpt_transformer_block_b200 as gb
-    H, Hk, B, T, P = s["heads"], s["kv_heads"], s["batch"], s["T_max"], s["max_prefix"]
+    H, Hk, B = s["heads"], s["kv_heads"], s["batch"]
     o = torch.empty_like(s["q"])
     lse = torch.empty(B, H, dtype=torch.float32, device="cuda")
-    ws = torch.empty(gb.gptb_prefix_decode_workspace_bytes(B, H, Hk, s["groups"], P, T), dtype=torch.uint8, device="cuda")
-    gb.gptb_prefix_decode_attention(s["q"], s["kp"], s["vp"], s["cu_prefix"], P, s["cu_group"], s["k"], s["v"], s["lens"],
-                                    o, lse, B, H, Hk, s["window"], ws)
+    ws = torch.empty(gb.gptb_prefix_decode_workspace_bytes(B, H, Hk), dtype=torch.uint8, device="cuda")
+    gb.gptb_prefix_decode_attention(s["q"], s["kp"], s["vp"], s["cu_prefix"], s["cu_group"], s["k"], s["v"], s["lens"], o, lse,
+                                    H, Hk, s["window"], ws)
     return {"o": o, "lse": lse}
 
 
