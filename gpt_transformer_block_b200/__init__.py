@@ -28,6 +28,9 @@ EXPORTS = [
     "gptb_muon_workspace_bytes", "gptb_muon_step", "gptb_muon_batched_workspace_bytes", "gptb_muon_step_batched",
     "gptb_gemm_bf16_batched", "gpt_stack_step_hooked", "gptb_cast_f32_bf16",
     "gptb_cast_bf16_f32", "gptb_decode_workspace_bytes", "gptb_gemm_fp8_workspace_bytes", "gptb_gemm_fp8",
+    "gptb_packed_attention", "gptb_packed_attention_workspace_bytes", "gptb_packed_attention_backward",
+    "gptb_prefix_decode_workspace_bytes", "gptb_prefix_decode_attention",
+    "gptb_policy_loss_workspace_bytes", "gptb_policy_loss", "gptb_token_logprobs",
 ]
 
 GRADS_READY_FN = ctypes.CFUNCTYPE(None, ctypes.c_int, ctypes.c_void_p)
@@ -134,7 +137,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                                            ctypes.c_longlong, ctypes.c_longlong, _vp, ctypes.c_int,
                                            ctypes.c_longlong, ctypes.c_longlong, ctypes.c_int, ctypes.c_int,
                                            ctypes.c_int, ctypes.c_int, _vp]
+    ll, ci, cf = ctypes.c_longlong, ctypes.c_int, ctypes.c_float
+    lib.gptb_packed_attention.argtypes = [_vp, ll, _vp, ll, _vp, ll, _vp, _vp, ll, _vp, ci, ci, ci, ci, ci, _vp]
+    lib.gptb_packed_attention_workspace_bytes.argtypes = [ci, ci]
+    lib.gptb_packed_attention_workspace_bytes.restype = ctypes.c_size_t
+    lib.gptb_packed_attention_backward.argtypes = [_vp, ll, _vp, ll, _vp, ll, _vp, ll, _vp, ll, _vp, _vp, _vp, ll, _vp,
+                                                   ll, _vp, ll, ci, ci, ci, ci, ci, _vp, ctypes.c_size_t, _vp]
+    lib.gptb_prefix_decode_workspace_bytes.argtypes = [ci, ci, ci]
+    lib.gptb_prefix_decode_workspace_bytes.restype = ctypes.c_size_t
+    lib.gptb_prefix_decode_attention.argtypes = [_vp, _vp, _vp, ll, _vp, ci, _vp, ci, _vp, _vp, _vp, ci, _vp, _vp, ci,
+                                                 ci, ci, ci, _vp, ctypes.c_size_t, _vp]
+    lib.gptb_policy_loss_workspace_bytes.argtypes = [ci]
+    lib.gptb_policy_loss_workspace_bytes.restype = ctypes.c_size_t
+    lib.gptb_policy_loss.argtypes = [_vp, ll, ci, ci, ci, _vp, _vp, _vp, _vp, _vp, cf, cf, cf, _vp, ll, _vp, _vp, _vp,
+                                     ctypes.c_size_t, _vp]
+    lib.gptb_token_logprobs.argtypes = [_vp, ll, ci, ci, ci, _vp, _vp, _vp]
     for name in EXPORTS:
+        if name.endswith("_workspace_bytes"):
+            continue
         if name not in ("gptb_workspace_bytes", "gptb_error_string", "gptb_reset_counters",
                         "gptb_launch_count", "gptb_polar_express_workspace_bytes", "gptb_muon_workspace_bytes",
                         "gptb_decode_workspace_bytes", "gptb_gemm_fp8_workspace_bytes",
@@ -370,6 +390,148 @@ def gptb_decode_attention(q, k_cache, v_cache, lens, o, lse, B, H, Hkv, T_max, w
     _check(load().gptb_decode_attention(ptr(q), ptr(k_cache), ptr(v_cache), ptr(lens), ptr(o), ptr(lse), int(B),
                                         int(H), int(Hkv), int(T_max), int(window), ptr(workspace), nbytes,
                                         _stream(stream)), "gptb_decode_attention")
+
+
+def _rows(name: str, t, cols: int, dtype, device, rows=None):
+    """t as a [rows, >= cols] device matrix with contiguous rows: (address, row stride)."""
+    if t.dim() != 2 or t.shape[1] < cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted [{'rows' if rows is None else rows}, {cols}]")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: its rows have to be contiguous")
+    _like(name, t, dtype, device)
+    # (one row has no stride to speak of)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _like(name: str, t, dtype, device):
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, wanted {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: a tensor of device memory is wanted, not on {t.device}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, wanted {device}")
+
+
+def _flat(name: str, t, dtype, device, count: int):
+    """t as a contiguous device array of count elements: its address."""
+    _like(name, t, dtype, device)
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {count} contiguous elements")
+    return t.data_ptr()
+
+
+def _workspace(t, device):
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace: contiguous memory of {device} is wanted")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _enqueue(device, fn, args, stream, what: str):
+    """fn(*args, stream) with the tensors' device as the current one; stream: that device's current one by default."""
+    import torch
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, _stream(stream)), what)
+    with torch.cuda.device(device):
+        _check(fn(*args, _stream(stream)), what)
+
+
+def gptb_packed_attention(q, k, v, cu_seqlens, o, lse, H, Hkv, window=-1, stream=None):
+    """Causal attention over packed sequences: q, o [total, H*128], k, v [total, Hkv*128] bf16 (column ranges of a
+    wider array are fine), cu_seqlens int32 [n_seq+1], lse fp32 [H, total]; all on one device."""
+    import torch
+    bf, dev, H, Hkv = torch.bfloat16, q.device, int(H), int(Hkv)
+    n = q.shape[0]
+    args = (*_rows("q", q, H * 128, bf, dev), *_rows("k", k, Hkv * 128, bf, dev, n),
+            *_rows("v", v, Hkv * 128, bf, dev, n), _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
+            *_rows("o", o, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n), n,
+            cu_seqlens.numel() - 1, H, Hkv, int(window))
+    _enqueue(dev, load().gptb_packed_attention, args, stream, "gptb_packed_attention")
+
+
+def gptb_packed_attention_workspace_bytes(total: int, H: int) -> int:
+    return int(load().gptb_packed_attention_workspace_bytes(int(total), int(H)))
+
+
+def gptb_packed_attention_backward(q, k, v, o, dout, lse, cu_seqlens, dq, dk, dv, H, Hkv, window, workspace,
+                                   stream=None):
+    """Gradients dq, dk, dv (bf16, overwritten) of gptb_packed_attention from dout and its o and lse."""
+    import torch
+    bf, dev, H, Hkv = torch.bfloat16, q.device, int(H), int(Hkv)
+    n = q.shape[0]
+    args = (*_rows("q", q, H * 128, bf, dev), *_rows("k", k, Hkv * 128, bf, dev, n),
+            *_rows("v", v, Hkv * 128, bf, dev, n), *_rows("o", o, H * 128, bf, dev, n),
+            *_rows("dout", dout, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n),
+            _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
+            *_rows("dq", dq, H * 128, bf, dev, n), *_rows("dk", dk, Hkv * 128, bf, dev, n),
+            *_rows("dv", dv, Hkv * 128, bf, dev, n), n, cu_seqlens.numel() - 1, H, Hkv, int(window),
+            *_workspace(workspace, dev))
+    _enqueue(dev, load().gptb_packed_attention_backward, args, stream, "gptb_packed_attention_backward")
+
+
+def gptb_prefix_decode_workspace_bytes(B: int, H: int, Hkv: int) -> int:
+    return int(load().gptb_prefix_decode_workspace_bytes(int(B), int(H), int(Hkv)))
+
+
+def gptb_prefix_decode_attention(q, k_prefix, v_prefix, cu_prefix, cu_group, k_cache, v_cache, lens, o, lse, H, Hkv,
+                                 window, workspace, stream=None):
+    """One decode step of sequences that share prompts: q, o [B, H, 128], k_prefix, v_prefix [rows, Hkv*128] (packed
+    prompts; a common row stride), cu_prefix, cu_group int32 [n_groups+1], k_cache, v_cache [B, T_max, Hkv, 128], lens
+    int32 [B], lse fp32 [B, H] or None."""
+    import torch
+    bf, i32, dev, H, Hkv = torch.bfloat16, torch.int32, q.device, int(H), int(Hkv)
+    B, T = k_cache.shape[0], k_cache.shape[1]
+    kp, ld = _rows("k_prefix", k_prefix, Hkv * 128, bf, dev)
+    vp, ldv = _rows("v_prefix", v_prefix, Hkv * 128, bf, dev, k_prefix.shape[0])
+    if ld != ldv and k_prefix.shape[0] > 1:
+        raise ValueError("k_prefix and v_prefix have to have the same row stride")
+    if cu_prefix.numel() != cu_group.numel():
+        raise ValueError("cu_prefix and cu_group have to have the same length")
+    args = (_flat("q", q, bf, dev, B * H * 128), kp, vp, max(ld, ldv), _flat("cu_prefix", cu_prefix, i32, dev, cu_prefix.numel()),
+            k_prefix.shape[0], _flat("cu_group", cu_group, i32, dev, cu_prefix.numel()), max(0, cu_prefix.numel() - 1),
+            _flat("k_cache", k_cache, bf, dev, B * T * Hkv * 128), _flat("v_cache", v_cache, bf, dev, B * T * Hkv * 128),
+            _flat("lens", lens, i32, dev, B), T, _flat("o", o, bf, dev, B * H * 128),
+            None if lse is None else _flat("lse", lse, torch.float32, dev, B * H), B, H, Hkv, int(window),
+            *_workspace(workspace, dev))
+    _enqueue(dev, load().gptb_prefix_decode_attention, args, stream, "gptb_prefix_decode_attention")
+
+
+def gptb_policy_loss_workspace_bytes(rows: int) -> int:
+    return int(load().gptb_policy_loss_workspace_bytes(int(rows)))
+
+
+def _logits_dtype(t) -> int:
+    import torch
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits: {t.dtype}, wanted bfloat16 or float32")
+    return BF16 if t.dtype == torch.bfloat16 else F32
+
+
+def gptb_policy_loss(logits, actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, dlogits, logp,
+                     stats, workspace, stream=None):
+    """Clipped policy loss with a KL term on logits [rows, vocab] (bf16 or fp32): stats fp32 [3] gets (loss, KL, clipped
+    weight), logp fp32 [rows] the tokens' log-probabilities, dlogits (None, another array or the logits themselves) the
+    gradient."""
+    import torch
+    f32, dev, (n, V) = torch.float32, logits.device, logits.shape
+    dt = _logits_dtype(logits)
+    z, ld = _rows("logits", logits, V, logits.dtype, dev)
+    dz, ldd = (None, 0) if dlogits is None else _rows("dlogits", dlogits, V, logits.dtype, dev, n)
+    args = (z, ld, dt, n, V, _flat("actions", actions, torch.int32, dev, n), _flat("weights", weights, f32, dev, n),
+            _flat("advantages", advantages, f32, dev, n), _flat("logp_old", logp_old, f32, dev, n),
+            None if logp_ref is None else _flat("logp_ref", logp_ref, f32, dev, n), float(clip_lo), float(clip_hi),
+            float(beta), dz, ldd, _flat("logp", logp, f32, dev, n), _flat("stats", stats, f32, dev, 3),
+            *_workspace(workspace, dev))
+    _enqueue(dev, load().gptb_policy_loss, args, stream, "gptb_policy_loss")
+
+
+def gptb_token_logprobs(logits, tokens, logp, stream=None):
+    """logp[i] = log softmax(logits[i])[tokens[i]] of logits [rows, vocab] (bf16 or fp32)."""
+    import torch
+    dev, (n, V) = logits.device, logits.shape
+    dt = _logits_dtype(logits)
+    args = (*_rows("logits", logits, V, logits.dtype, dev), dt, n, V, _flat("tokens", tokens, torch.int32, dev, n),
+            _flat("logp", logp, torch.float32, dev, n))
+    _enqueue(dev, load().gptb_token_logprobs, args, stream, "gptb_token_logprobs")
 
 
 def gptb_device_error(stream=None) -> int:

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libgptblock.so")
 SOURCES = ["api.cu"]
 DEPS = ["api.cu", "common.cuh", "gemm.cuh", "attention.cuh", "attention_tc.cuh", "elementwise.cuh", "rows.cuh",
-        "decode.cuh"]
+        "decode.cuh", "packed_attention.cuh", "prefix_decode.cuh", "policy.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

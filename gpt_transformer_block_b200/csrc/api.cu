@@ -18,6 +18,9 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "elementwise.cuh"
+#include "packed_attention.cuh"
+#include "policy.cuh"
+#include "prefix_decode.cuh"
 #include "rows.cuh"
 #include "gemm.cuh"
 
@@ -1490,6 +1493,265 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
   return GPTB_OK;
 }
 
+// ------------------------------------------------- packed attention --
+
+namespace {
+
+// rows of a packed array: heads of 128 bf16 columns, `ld` elements from row to row
+bool packed_ok(const void* p, long long ld, int heads) {
+  return p && aligned16(p) && ld % 8 == 0 && ld >= (long long)heads * 128 && ld < (1ll << 36);
+}
+bool packed_shape_ok(const int32_t* cu, int total, int n_seq, int H, int Hkv, int window) {
+  return cu && total >= 0 && total <= (1 << 30) && n_seq >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && H <= (1 << 16) &&
+         window >= -1;
+}
+bool packed_map(CUtensorMap* m, const void* p, int heads, int total, long long ld, int box_rows) {
+  return make_tmap(m, p, false, (uint64_t)heads * 128, (uint64_t)total, (uint64_t)ld, 64, (uint32_t)box_rows);
+}
+size_t packed_dq_bytes(int total, int H) { return (size_t)total * H * 128 * sizeof(float); }
+
+}  // namespace
+
+int gptb_packed_attention(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                          const int32_t* cu_seqlens, void* o, long long ldo, float* lse, int total, int n_seq, int H,
+                          int Hkv, int window, gptb_stream_t stream) {
+  if (!packed_shape_ok(cu_seqlens, total, n_seq, H, Hkv, window)) return GPTB_ERR_INVALID_ARG;
+  if (total == 0) return GPTB_OK;  // (empty arrays may have no address)
+  if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) || !lse)
+    return GPTB_ERR_INVALID_ARG;
+  const long long grid = (long long)((total + FA_QB - 1) / FA_QB) * H;
+  if (grid > INT_MAX) return GPTB_ERR_UNSUPPORTED;
+  if (n_seq == 0) return GPTB_OK;
+  if (dev_info().cc_major != 10) return GPTB_ERR_UNSUPPORTED;
+  CUtensorMap tq, tk, tv, to;
+  if (!packed_map(&tq, q, H, total, ldq, 128) || !packed_map(&tk, k, Hkv, total, ldk, 128) ||
+      !packed_map(&tv, v, Hkv, total, ldv, 128) || !packed_map(&to, o, H, total, ldo, 32))
+    return GPTB_ERR_CUDA;
+  CK(cudaFuncSetAttribute(packed_attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FA_SMEM));
+  packed_attn_fwd_kernel<<<(unsigned)grid, FA_THREADS, FA_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(
+      tq, tk, tv, to, static_cast<bf16*>(o), ldo, lse, cu_seqlens, n_seq, total, H, Hkv, window);
+  CKL();
+  return GPTB_OK;
+}
+
+size_t gptb_packed_attention_workspace_bytes(int total, int H) {
+  if (total < 0 || H <= 0) return 0;
+  return packed_dq_bytes(total, H) + (size_t)total * H * sizeof(float) + 256;
+}
+
+int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, long long ldk, const void* v,
+                                   long long ldv, const void* o, long long ldo, const void* dout, long long lddo,
+                                   const float* lse, const int32_t* cu_seqlens, void* dq, long long lddq, void* dk,
+                                   long long lddk, void* dv, long long lddv, int total, int n_seq, int H, int Hkv,
+                                   int window, void* workspace, size_t workspace_bytes, gptb_stream_t stream) {
+  if (!packed_shape_ok(cu_seqlens, total, n_seq, H, Hkv, window)) return GPTB_ERR_INVALID_ARG;
+  if (total == 0) return GPTB_OK;  // (empty arrays may have no address)
+  if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) ||
+      !packed_ok(dout, lddo, H) || !packed_ok(dq, lddq, H) || !packed_ok(dk, lddk, Hkv) || !packed_ok(dv, lddv, Hkv) ||
+      !lse || !workspace || !aligned16(workspace))
+    return GPTB_ERR_INVALID_ARG;
+  if (workspace_bytes < gptb_packed_attention_workspace_bytes(total, H)) return GPTB_ERR_WORKSPACE;
+  const long long grid = (long long)((total + AB2_BK - 1) / AB2_BK) * Hkv;
+  if (grid > INT_MAX) return GPTB_ERR_UNSUPPORTED;
+  if (n_seq == 0) return GPTB_OK;
+  if (dev_info().cc_major != 10) return GPTB_ERR_UNSUPPORTED;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  float* acc = static_cast<float*>(workspace);
+  float* D = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + packed_dq_bytes(total, H));
+  CUtensorMap tq, tk, tv, tdo, tdk, tdv;
+  if (!packed_map(&tq, q, H, total, ldq, 64) || !packed_map(&tk, k, Hkv, total, ldk, 128) ||
+      !packed_map(&tv, v, Hkv, total, ldv, 128) || !packed_map(&tdo, dout, H, total, lddo, 64) ||
+      !packed_map(&tdk, dk, Hkv, total, lddk, 32) || !packed_map(&tdv, dv, Hkv, total, lddv, 32))
+    return GPTB_ERR_CUDA;
+  const long long sms = dev_info().sms;
+  const auto blocks = [&](long long n) { return (int)std::max(1ll, std::min((n + 255) / 256, sms * 8)); };
+  packed_attn_pre_kernel<<<blocks((long long)total * H * 32), 256, 0, st>>>(
+      static_cast<const bf16*>(o), ldo, static_cast<const bf16*>(dout), lddo, D, acc, cu_seqlens, n_seq, total, H);
+  CKL();
+  CK(cudaFuncSetAttribute(packed_attn_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB2_SMEM));
+  packed_attn_bwd_kernel<<<(unsigned)grid, AB2_THREADS, AB2_SMEM, st>>>(
+      tq, tk, tv, tdo, tdk, tdv, static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, lse, D, acc, cu_seqlens,
+      n_seq, total, H, Hkv, window);
+  CKL();
+  packed_attn_dq_kernel<<<blocks((long long)total * H * 16), 256, 0, st>>>(acc, static_cast<bf16*>(dq), lddq, cu_seqlens,
+                                                                           n_seq, total, H);
+  CKL();
+  return GPTB_OK;
+}
+
+// ---------------------------------------------------- prefix decode --
+
+namespace {
+
+struct PrefixWs {
+  size_t plan, rec_a, rec_b, bytes;
+};
+int prefix_spt(int B, int G) { return std::max(1, std::min(128 / G, B)); }
+PrefixWs prefix_ws(int B, int H, int Hkv) {
+  PrefixWs w;
+  const int G = H / Hkv;
+  w.plan = 0;
+  w.rec_a = (((size_t)B + 1) * sizeof(int4) + 255) / 256 * 256;
+  w.rec_b = w.rec_a + (size_t)2 * B * H * 2 * PD_REC * sizeof(float);
+  w.bytes = w.rec_b + (size_t)PD_MAX_CTAS * prefix_spt(B, G) * G * 2 * PD_REC * sizeof(float);
+  return w;
+}
+
+}  // namespace
+
+size_t gptb_prefix_decode_workspace_bytes(int B, int H, int Hkv) {
+  if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv || H / Hkv > 128) return 0;
+  return prefix_ws(B, H, Hkv).bytes;
+}
+
+int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void* v_prefix, long long ld_prefix,
+                                 const int32_t* cu_prefix, int total_prefix, const int32_t* cu_group, int n_groups,
+                                 const void* k_cache, const void* v_cache, const int32_t* lens, int T_max, void* o,
+                                 float* lse, int B, int H, int Hkv, int window, void* workspace,
+                                 size_t workspace_bytes, gptb_stream_t stream) {
+  if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv || T_max <= 0 || total_prefix < 0 || n_groups < 0 || window < -1)
+    return GPTB_ERR_INVALID_ARG;
+  if (B == 0) return GPTB_OK;  // (empty arrays may have no address)
+  if (!q || !k_cache || !v_cache || !lens || !o) return GPTB_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return GPTB_ERR_INVALID_ARG;
+  if (n_groups > 0 && (!cu_prefix || !cu_group)) return GPTB_ERR_INVALID_ARG;
+  if (n_groups > 0 && total_prefix > 0 && (!packed_ok(k_prefix, ld_prefix, Hkv) || !packed_ok(v_prefix, ld_prefix, Hkv)))
+    return GPTB_ERR_INVALID_ARG;
+  if (H / Hkv > 128) return GPTB_ERR_UNSUPPORTED;
+  const long long tiles = (long long)B * Hkv * ((T_max + 127) / 128 + ((long long)total_prefix + 127) / 128);
+  if (tiles > (1ll << 30) || (long long)B * T_max > (1ll << 30) || (long long)B * H > (1ll << 30) ||
+      total_prefix > (1 << 30))
+    return GPTB_ERR_UNSUPPORTED;
+  if (!workspace || !aligned16(workspace)) return GPTB_ERR_INVALID_ARG;
+  if (workspace_bytes < gptb_prefix_decode_workspace_bytes(B, H, Hkv)) return GPTB_ERR_WORKSPACE;
+  if (dev_info().cc_major != 10) return GPTB_ERR_UNSUPPORTED;
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return GPTB_ERR_CUDA;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int G = H / Hkv;
+  const bool prefix = n_groups > 0 && total_prefix > 0;
+  PrefixArgs a;
+  a.cu_prefix = cu_prefix;
+  a.cu_group = cu_group;
+  a.lens = lens;
+  a.total_prefix = prefix ? total_prefix : 0;
+  a.n_groups = n_groups;
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.T_max = T_max;
+  a.window = window;
+  a.spt = prefix_spt(B, G);
+  const PrefixWs w = prefix_ws(B, H, Hkv);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.plan = reinterpret_cast<int4*>(ws + w.plan);
+  a.rec_a = reinterpret_cast<float*>(ws + w.rec_a);
+  a.rec_b = reinterpret_cast<float*>(ws + w.rec_b);
+  // query rows of one kv head: [sequences][G heads][64 columns] boxes of q [B][H][128]
+  CUtensorMap tqp, tqo, tkp, tvp, tko, tvo;
+  const auto q_map = [&](CUtensorMap* m, int seqs) {
+    cuuint64_t dims[3] = {128, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[2] = {256, (cuuint64_t)H * 256};
+    cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)seqs};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  const long long ld_own = (long long)Hkv * 128;
+  if (!q_map(&tqp, a.spt) || !q_map(&tqo, 1) || !packed_map(&tko, k_cache, Hkv, B * T_max, ld_own, PD_BOX) ||
+      !packed_map(&tvo, v_cache, Hkv, B * T_max, ld_own, PD_BOX))
+    return GPTB_ERR_CUDA;
+  tkp = tko;
+  tvp = tvo;
+  if (prefix && (!packed_map(&tkp, k_prefix, Hkv, total_prefix, ld_prefix, PD_BOX) ||
+                 !packed_map(&tvp, v_prefix, Hkv, total_prefix, ld_prefix, PD_BOX)))
+    return GPTB_ERR_CUDA;
+  const int grid = (int)std::max(1ll, std::min<long long>(tiles, std::min(dev_info().sms, PD_MAX_CTAS)));
+  CK(cudaFuncSetAttribute(prefix_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PD_SMEM));
+  prefix_split_kernel<<<grid, PD_THREADS, PD_SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, a);
+  CKL();
+  prefix_combine_kernel<<<(unsigned)(((long long)B * H + 3) / 4), 128, 0, st>>>(a, static_cast<bf16*>(o), lse, grid);
+  CKL();
+  return GPTB_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ policy loss --
+
+namespace {
+
+// CTAs of the row kernel: two to an SM
+int policy_ctas(int rows) { return std::max(1, std::min(rows, std::min(512, std::max(1, dev_info().sms) * 2))); }
+
+template <class T>
+int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, cudaStream_t st) {
+  constexpr int VEC = 16 / (int)sizeof(T);
+  const bool vec = aligned16(logits) && a.ld % VEC == 0 && (!dlogits || (aligned16(dlogits) && a.ldd % VEC == 0));
+  const int grid = policy_ctas(a.rows);
+  if (vec)
+    policy_rows_kernel<T, VEC><<<grid, POL_THREADS, 0, st>>>(static_cast<const T*>(logits), static_cast<T*>(dlogits), a);
+  else
+    policy_rows_kernel<T, 1><<<grid, POL_THREADS, 0, st>>>(static_cast<const T*>(logits), static_cast<T*>(dlogits), a);
+  CKL();
+  return GPTB_OK;
+}
+bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+int policy_shape(const void* logits, long long ld, int dtype, int rows, int vocab) {
+  if (dtype != GPTB_F32 && dtype != GPTB_BF16) return GPTB_ERR_UNSUPPORTED;
+  if (rows < 0 || vocab < 1 || vocab > (1 << 30) || ld < vocab || ld >= (1ll << 36)) return GPTB_ERR_INVALID_ARG;
+  // (empty arrays may have no address)
+  if (rows > 0 && (!logits || !aligned_to(logits, dtype == GPTB_F32 ? 4 : 2))) return GPTB_ERR_INVALID_ARG;
+  return GPTB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t gptb_policy_loss_workspace_bytes(int rows) {
+  if (rows < 0) return 0;
+  return (size_t)std::min(rows, 512) * 3 * sizeof(double) + 256;
+}
+
+int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
+                     const float* weights, const float* advantages, const float* logp_old, const float* logp_ref,
+                     float clip_lo, float clip_hi, float beta, void* dlogits, long long ldd, float* logp, float* stats,
+                     void* workspace, size_t workspace_bytes, gptb_stream_t stream) {
+  TRY(policy_shape(logits, ld, dtype, rows, vocab));
+  if (!(clip_lo >= 0.f && clip_lo <= 1.f) || !(clip_hi >= 0.f) || !std::isfinite(beta)) return GPTB_ERR_INVALID_ARG;
+  if (!stats) return GPTB_ERR_INVALID_ARG;
+  if (rows > 0 && (!actions || !weights || !advantages || !logp_old || !logp || (beta != 0.f && !logp_ref)))
+    return GPTB_ERR_INVALID_ARG;
+  if (dlogits && (ldd < vocab || ldd >= (1ll << 36) || !aligned_to(dlogits, dtype == GPTB_F32 ? 4 : 2) ||
+                  (dlogits == logits && ldd != ld)))
+    return GPTB_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace)) return GPTB_ERR_INVALID_ARG;
+  if (workspace_bytes < gptb_policy_loss_workspace_bytes(rows)) return GPTB_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    CK(cudaMemsetAsync(stats, 0, 3 * sizeof(float), st));
+    return GPTB_OK;
+  }
+  PolicyArgs a{actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, logp,
+               static_cast<double*>(workspace), ld, ldd, rows, vocab};
+  TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, st) : policy_launch<bf16>(logits, dlogits, a, st));
+  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, policy_ctas(rows), stats);
+  CKL();
+  return GPTB_OK;
+}
+
+int gptb_token_logprobs(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* tokens,
+                        float* logp, gptb_stream_t stream) {
+  TRY(policy_shape(logits, ld, dtype, rows, vocab));
+  if (rows == 0) return GPTB_OK;
+  if (!tokens || !logp) return GPTB_ERR_INVALID_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  PolicyArgs a{tokens, nullptr, nullptr, nullptr, nullptr, 0.f, 0.f, 0.f, logp, nullptr, ld, 0, rows, vocab};
+  return dtype == GPTB_F32 ? policy_launch<float>(logits, nullptr, a, st) : policy_launch<bf16>(logits, nullptr, a, st);
+}
+
 int gptb_cast_f32_bf16(const float* x, void* y, long long n, float scale, gptb_stream_t stream) {
   if (!x || !y || n < 0) return GPTB_ERR_INVALID_ARG;
   if (n == 0) return GPTB_OK;
@@ -1614,7 +1876,7 @@ const char* gptb_error_string(int code) {
     case GPTB_ERR_CUDA: return "CUDA error";
     case GPTB_ERR_TIMEOUT: return "bounded device wait expired";
     case GPTB_ERR_WORKSPACE: return "workspace too small";
-    case GPTB_ERR_BAD_INPUT: return "invalid input data found on the device (a target outside [0, vocab))";
+    case GPTB_ERR_BAD_INPUT: return "invalid input data found on the device (a target outside [0, vocab), bad sequence offsets)";
     default: return "unknown error";
   }
 }

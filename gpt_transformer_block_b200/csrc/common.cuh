@@ -30,7 +30,8 @@ enum : int {
   ERRW_TIMEOUT_DRAIN = 0x104,
   ERRW_TIMEOUT_PROBE = 0x105,
   // invalid input data found on the device (codes 0x2xx)
-  ERRW_BAD_TARGET = 0x201,  // a cross-entropy target outside [0, vocab)
+  ERRW_BAD_TARGET = 0x201,  // a cross-entropy target or an action outside [0, vocab)
+  ERRW_BAD_OFFSETS = 0x202,  // sequence offsets that decrease or leave their array
 };
 
 __device__ __forceinline__ void record_error(int code) { atomicCAS(&g_error_word, 0, code); }

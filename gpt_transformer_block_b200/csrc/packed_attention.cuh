@@ -1,0 +1,780 @@
+// Causal grouped-query attention over packed sequences of different lengths
+// (bf16, hd = 128), forward and backward, on the 5th-generation tensor cores.
+//
+// The rows of all sequences lie one after the other; cu[s] .. cu[s+1]-1 are
+// those of sequence s.  Row t of sequence s sees the rows
+//   vis(t) = { j : cu[s] <= j <= t and (W < 0 or t - j <= W) }
+//   S = q k^T / sqrt(hd), lse = log sum_vis exp S, P = exp(S - lse), o = P v
+//   D = rowsum(dO o), dS = P (dO v^T - D) / sqrt(hd)
+//   dq = dS k, dk = sum over the group's heads of dS^T q, dv = ... of P^T dO
+//
+// Tiles are cut out of the packed rows, not out of the sequences: a tile may
+// hold the end of one sequence and several short ones, each row carries its
+// own visible range, and only the tiles that some row sees are visited.  So
+// the grid needs neither the lengths nor a plan made from them (they stay on
+// the device), and short sequences share tiles instead of padding one each.
+// Products with P = 0 are part of the matrix products, so a NaN or infinity in
+// a row reaches the rows that share a tile with it; what lies behind the last
+// sequence reaches nothing.
+//
+// The tile schedules are those of attention_tc.cuh: forward 256 queries of one
+// head per CTA over 128-key tiles, backward 128 keys of one kv head per CTA
+// over 64-query tiles; D, and the zeroing of the fp32 dQ sums, in a pass of
+// its own before, the rounding of dQ to bf16 in one after.
+#pragma once
+#include "attention_tc.cuh"
+#include "common.cuh"
+
+namespace gptb {
+
+// rows that belong to sequences, inside the arrays whatever cu holds
+__device__ __forceinline__ int packed_rows(const int32_t* __restrict__ cu, int n_seq, int total) {
+  return max(0, min(cu[n_seq], total));
+}
+
+// first row and end of the sequence that holds row t < n_rows (found by
+// bisection; t itself lies inside the result whatever cu holds)
+__device__ __forceinline__ int2 packed_seq(const int32_t* __restrict__ cu, int n_seq, int t, int n_rows) {
+  int lo = 0, hi = n_seq;  // cu[lo] <= t < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t) lo = mid; else hi = mid;
+  }
+  return make_int2(max(0, min(cu[lo], t)), min(max(cu[hi], t + 1), n_rows));
+}
+
+// offsets that are not 0 = cu[0] <= cu[1] <= ... <= total are reported (one CTA calls this)
+__device__ __forceinline__ void packed_check(const int32_t* __restrict__ cu, int n_seq, int total) {
+  for (int s = threadIdx.x; s <= n_seq; s += blockDim.x) {
+    const int c = cu[s];
+    if ((s == 0 && c != 0) || (s > 0 && cu[s - 1] > c) || c > total) record_error(ERRW_BAD_OFFSETS);
+  }
+}
+
+// one row (two 128-byte halves `half` bytes apart) of a swizzled tile
+__device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * half + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+}
+
+__global__ void __launch_bounds__(FA_THREADS, 1)
+    packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                           bf16* __restrict__ o, long long ldo, float* __restrict__ lse,
+                           const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window) {
+  extern __shared__ uint8_t fa_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fa_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;                // 2 query tiles
+  uint8_t* sK = sQ + 2 * FA_TILE;    // 2 stages
+  uint8_t* sV = sK + 2 * FA_TILE;    // 2 stages
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * FA_TILE);
+  uint64_t* q_full = bars + 0;
+  uint64_t* k_full = bars + 1;    // [2 slots]
+  uint64_t* k_empty = bars + 3;   // [2 slots]
+  uint64_t* v_full = bars + 5;    // [2 slots]
+  uint64_t* v_empty = bars + 7;   // [2 slots]
+  uint64_t* s_full = bars + 9;    // [2 query tiles] S_t of the next key tile computed
+  uint64_t* p_full = bars + 11;   // [2 query tiles] P_t written (one arrival per softmax warp)
+  uint64_t* o_done = bars + 13;   // [2 query tiles] O_t += P_t V_j done
+  uint64_t* drain = bars + 15;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  __shared__ int s_lo[2];  // first visible row of the first query of each query tile
+
+  // one CTA per (256 consecutive packed rows, head), the last rows first: the
+  // end of a long sequence is its heaviest part
+  const int nqb = (total + FA_QB - 1) / FA_QB;
+  const int qb = nqb - 1 - (int)blockIdx.x / H;
+  const int h = (int)blockIdx.x % H;
+  const int kvh = h / (H / Hkv);
+  const int q0 = qb * FA_QB;
+  const int n_rows = packed_rows(cu, n_seq, total);
+  if (blockIdx.x == 0) packed_check(cu, n_seq, total);
+  if (q0 >= n_rows) return;  // (the whole CTA: rows behind the last sequence)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_o);
+  }
+  // a softmax thread's query row sees the packed rows kv_lo .. kv_hi
+  int tq = 0, kv_lo = 0, kv_hi = -1;
+  if (warp >= 2) {
+    tq = q0 + ((warp - 2) >> 2) * FA_BM + (warp & 3) * 32 + lane;
+    if (tq < n_rows) {
+      kv_lo = packed_seq(cu, n_seq, tq, n_rows).x;
+      if (window >= 0) kv_lo = max(kv_lo, tq - window);
+      kv_hi = tq;
+    }
+    if ((tq & (FA_BM - 1)) == 0) s_lo[(warp - 2) >> 2] = tq < n_rows ? kv_lo : tq;
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // key tiles that intersect the visible keys of query tile t (none past the
+  // last row); both ranges are monotone in t and overlap or touch, so their
+  // union is one range
+  int lo[2], hi[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int qt = q0 + t * FA_BM;
+    lo[t] = max(s_lo[t], s_lo[0]) / FA_BN;
+    hi[t] = (qt < n_rows) ? min(qt + FA_BM - 1, n_rows - 1) / FA_BN : lo[t] - 1;
+  }
+  const int jlo = lo[0];
+  const int jhi = max(hi[0], hi[1]);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int nq = (hi[1] >= lo[1]) ? 2 : 1;
+      mbar_arrive_expect_tx(q_full, nq * FA_TILE);
+      for (int t = 0; t < nq; ++t) {
+        tma_load_2d(sQ + t * FA_TILE, &tm_q, q_full, h * 128, q0 + t * FA_BM);
+        tma_load_2d(sQ + t * FA_TILE + 16384, &tm_q, q_full, h * 128 + 64, q0 + t * FA_BM);
+      }
+      for (int j = jlo; j <= jhi; ++j) {
+        const int i = j - jlo, st = i & 1;
+        const uint32_t par = ((i >> 1) & 1) ^ 1u;
+        const int kr = j * FA_BN;
+        if (!mbar_wait(&k_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&k_full[st], FA_TILE);
+        uint8_t* k = sK + st * FA_TILE;
+        tma_load_2d(k, &tm_k, &k_full[st], kvh * 128, kr);
+        tma_load_2d(k + 16384, &tm_k, &k_full[st], kvh * 128 + 64, kr);
+        if (!mbar_wait(&v_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&v_full[st], FA_TILE);
+        uint8_t* v = sV + st * FA_TILE;
+        tma_load_2d(v, &tm_v, &v_full[st], kvh * 128, kr);
+        tma_load_2d(v + 16384, &tm_v, &v_full[st], kvh * 128 + 64, kr);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t IDESC_S = make_idesc(128, 128, false, false, false);
+      constexpr uint32_t IDESC_O = make_idesc(128, 128, false, true, false);
+      bool ok = mbar_wait(q_full, 0, abort_flag, ERRW_TIMEOUT_MMA);
+      auto in = [&](int t, int j) { return j >= lo[t] && j <= hi[t]; };
+      // S_t for key tile j; the K slot is released after its last score product
+      auto issue_s = [&](int t, int j) -> bool {
+        const int i = j - jlo, st = i & 1;
+        if (!mbar_wait(&k_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        tc_fence_after();
+        const uint32_t aQ = smem_u32(sQ + t * FA_TILE), aK = smem_u32(sK + st * FA_TILE);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ss(tmem + t * 128, fa_desc_k(aQ, k), fa_desc_k(aK, k), IDESC_S, k > 0 ? 1u : 0u);
+        mma_commit(&s_full[t]);
+        if (t == 1 || !in(1, j)) mma_commit(&k_empty[st]);
+        return true;
+      };
+      // O_t += P_t V_j once the softmax has written P_t; the V slot is released after its last PV product
+      auto issue_pv = [&](int t, int j) -> bool {
+        const int i = j - jlo, st = i & 1;
+        const int c = j - lo[t];
+        if (!mbar_wait(&v_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        if (!mbar_wait(&p_full[t], c & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        tc_fence_after();
+        const uint32_t aV = smem_u32(sV + st * FA_TILE);
+        // A = P_t from TMEM (lane = query row, 8 columns per 16 keys)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, fa_desc_mn(aV, k), IDESC_O,
+                      (c > 0 || k > 0) ? 1u : 0u);
+        mma_commit(&o_done[t]);
+        if (t == 1 || !in(1, j)) mma_commit(&v_empty[st]);
+        return true;
+      };
+      if (ok && in(0, jlo)) ok = issue_s(0, jlo);
+      if (ok && hi[1] >= lo[1]) ok = issue_s(1, lo[1]);
+      for (int j = jlo; ok && j <= jhi; ++j) {
+        if (in(0, j)) {
+          ok = issue_pv(0, j) && (j + 1 > hi[0] || issue_s(0, j + 1));
+          if (!ok) break;
+        }
+        if (in(1, j)) ok = issue_pv(1, j) && (j + 1 > hi[1] || issue_s(1, j + 1));
+      }
+      if (*abort_flag) {
+        mma_commit(drain);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0))
+          if (globaltimer_ns() - t0 > 100000000ull) { record_error(ERRW_TIMEOUT_DRAIN); break; }
+      }
+    }
+  } else {
+    // softmax of query tile tt: TMEM lane quarter qw = warp % 4 -> rows 32*qw .. 32*qw+31
+    const int tt = (warp - 2) >> 2;
+    const int qw = warp & 3;
+    const int r = qw * 32 + lane;        // row within the query tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
+    const uint32_t s_col = (uint32_t)(tt * 128), o_col = (uint32_t)(256 + tt * 128);
+    const float sl2 = LOG2E / sqrtf(128.f);
+    const int qt0 = q0 + tt * FA_BM;  // first query of the tile
+    float m_used = -INFINITY, l = 0.f;
+    bool ok = true;
+    const int lo_t = tt ? lo[1] : lo[0];
+    const int n = (tt ? hi[1] : hi[0]) - lo_t + 1;  // key tiles of this query tile (0 past the last row)
+    for (int c = 0; c < n && ok; ++c) {
+      const int k0 = (lo_t + c) * FA_BN;
+      ok = mbar_wait_warp(&s_full[tt], c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        tmem_ld_32x32b_x32(lane_addr + s_col + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
+      tmem_ld_wait();
+      // rows are masked in a tile that reaches past the first query, or
+      // before what the last one sees (kv_lo grows with the row)
+      const bool need_mask = __any_sync(0xffffffffu, k0 < kv_lo || k0 + FA_BN - 1 > kv_hi);
+      if (need_mask) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) {
+          const int jk = k0 + i;
+          v[i] = (jk >= kv_lo && jk <= kv_hi) ? v[i] : __float_as_uint(-INFINITY);
+        }
+      }
+      float mp[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(v[i]);
+#pragma unroll
+      for (int i = 8; i < 128; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
+      const float mx =
+          fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])), fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+      // the running max moves only when it grows by more than 8 (base 2)
+      const bool grow = mx > m_used + 8.f;
+      const float corr = grow ? fast_exp2(m_used - mx) : 1.f;  // 0 when m_used is -inf
+      if (grow) {
+        l *= corr;
+        m_used = mx;
+      }
+      const float mu = (m_used == -INFINITY) ? 0.f : m_used;
+      // P = exp2(s*scale - m) as bf16 pairs (key 2c in the low half) over the
+      // first 64 columns of S_t
+      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int hq = 0; hq < 4; ++hq) {  // 32 keys (16 columns of P) at a time
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int i = hq * 32 + 2 * e;
+          const float p0 = fast_exp2(fmaf(__uint_as_float(v[i]), sl2, -mu));  // exp2(-inf) = 0 for masked keys
+          const float p1 = fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl2, -mu));
+          lp[(2 * e) & 3] += p0;
+          lp[(2 * e + 1) & 3] += p1;
+          pk[e] = pack_bf16(p0, p1);
+        }
+        tmem_st_32x32b_x16(lane_addr + s_col + hq * 16, pk);
+      }
+      l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      // V rows behind the last sequence may hold anything (0 * NaN is NaN):
+      // they are zeroed before the product that reads them.  Both groups write
+      // the same zeros.
+      if (n_rows < total && k0 + FA_BN > n_rows && c == n - 1) {
+        const int i = lo_t + c - jlo;
+        ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+        if (!ok) break;
+        if (k0 + r >= n_rows) zero_tile_row(sV + (i & 1) * FA_TILE, 16384, r);
+        fence_proxy_async_smem();
+      }
+      // O_t to the new max (the TMEM accesses are warp-collective: the whole
+      // warp enters, rows that keep their max use 1).  O_t holds every PV
+      // product up to key tile c-1 (the commit of S_t above follows them);
+      // the wait states it.
+      if (c > 0 && __any_sync(0xffffffffu, grow)) {
+        ok = mbar_wait_warp(&o_done[tt], (c - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k) {
+          uint32_t w[32];
+          tmem_ld_32x32b_x32(lane_addr + o_col + k * 32, w);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * corr);
+          tmem_st_32x32b_x32(lane_addr + o_col + k * 32, w);
+        }
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[tt]);
+    }
+    if (n > 0 && __all_sync(0xffffffffu, ok) &&
+        mbar_wait_warp(&o_done[tt], (n - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
+      tc_fence_after();
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      // O_t (bf16) leaves through the Q_t tile, free once every S_t product
+      // has completed (they precede the last PV_t that o_done follows): two
+      // 64-column halves of 128 rows x 128 bytes, 128-byte swizzle; a warp
+      // whose 32 rows all lie inside the sequences stores them with two TMA
+      // boxes, the last rows go out one by one
+      uint8_t* stg = sQ + tt * FA_TILE;
+      const int row0 = qt0 + qw * 32;  // first query of this warp's rows
+      const bool whole = row0 + 32 <= n_rows;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {  // columns 32k .. 32k+31
+        uint32_t w[32];
+        tmem_ld_32x32b_x32(lane_addr + o_col + k * 32, w);
+        tmem_ld_wait();
+        uint8_t* row = stg + (k >> 1) * 16384 + r * 128;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          uint4 u;
+          u.x = pack_bf16(__uint_as_float(w[g * 8 + 0]) * inv, __uint_as_float(w[g * 8 + 1]) * inv);
+          u.y = pack_bf16(__uint_as_float(w[g * 8 + 2]) * inv, __uint_as_float(w[g * 8 + 3]) * inv);
+          u.z = pack_bf16(__uint_as_float(w[g * 8 + 4]) * inv, __uint_as_float(w[g * 8 + 5]) * inv);
+          u.w = pack_bf16(__uint_as_float(w[g * 8 + 6]) * inv, __uint_as_float(w[g * 8 + 7]) * inv);
+          const int cg = (k & 1) * 4 + g;  // 16-byte chunk within the 128-byte half row
+          if (whole)
+            *reinterpret_cast<uint4*>(row + ((cg ^ (r & 7)) << 4)) = u;
+          else if (tq < n_rows)
+            *reinterpret_cast<uint4*>(o + (long long)tq * ldo + h * 128 + k * 32 + g * 8) = u;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && whole) {
+        tma_store_2d(&tm_o, stg + qw * 4096, h * 128, row0);
+        tma_store_2d(&tm_o, stg + 16384 + qw * 4096, h * 128 + 64, row0);
+        bulk_commit_group();
+        bulk_wait_read0();  // the tile's shared memory is read before the CTA ends
+      }
+      __syncwarp();
+      if (tq < n_rows) lse[(long long)h * total + tq] = (m_used + log2f(l)) * LN2;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+
+// Roles, TMEM columns and barriers as in attn_bwd_tc_kernel.
+__global__ void __launch_bounds__(AB2_THREADS, 1)
+    packed_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                           const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                           const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
+                           bf16* __restrict__ dk, long long lddk, bf16* __restrict__ dv, long long lddv,
+                           const float* __restrict__ lse, const float* __restrict__ Dd, float* __restrict__ dq,
+                           const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window) {
+  extern __shared__ uint8_t ab_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ab_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + AB2_KV_TILE;
+  uint8_t* sQ = sV + AB2_KV_TILE;                  // AB2_STAGES stages
+  uint8_t* sDO = sQ + AB2_STAGES * AB2_Q_TILE;     // AB2_STAGES stages
+  uint8_t* sDS = sDO + AB2_STAGES * AB2_Q_TILE;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sDS + AB2_PS_TILE);
+  uint64_t* kv_full = bars + 0;
+  uint64_t* qdo_full = bars + 1;                 // [AB2_STAGES] TMA bytes + one arrival after LSE / D are stored
+  uint64_t* qdo_empty = bars + 1 + AB2_STAGES;   // [AB2_STAGES]
+  uint64_t* s_full = bars + 1 + 2 * AB2_STAGES;
+  uint64_t* s_empty = s_full + 1;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* ds_free = s_full + 3;
+  uint64_t* dq_full = s_full + 4;
+  uint64_t* dq_free = s_full + 5;
+  uint64_t* acc_done = s_full + 6;
+  uint64_t* drain = s_full + 7;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(s_full + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* sLD = reinterpret_cast<float*>(bars + 32);  // [AB2_STAGES][lse*log2e 64 | D 64]
+
+  __shared__ int s_vis[2];  // last query that sees the tile's first key; ... its last key
+
+  const int kb = (int)blockIdx.x / Hkv, kvh = (int)blockIdx.x % Hkv;
+  const int G = H / Hkv;
+  const int k0 = kb * AB2_BK;
+  const int n_rows = packed_rows(cu, n_seq, total);
+  if (k0 >= n_rows) return;  // (the whole CTA: rows behind the last sequence)
+  const long long lddq = (long long)H * 128;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int i = 0; i < AB2_STAGES; ++i) {
+      mbar_init(&qdo_full[i], 2);
+      mbar_init(&qdo_empty[i], 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, 8);
+    mbar_init(p_full, 8);
+    mbar_init(ds_free, 1);
+    mbar_init(dq_full, 1);
+    mbar_init(dq_free, 8);
+    mbar_init(acc_done, 1);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    tma_prefetch_desc(&tm_do);
+    tma_prefetch_desc(&tm_dk);
+    tma_prefetch_desc(&tm_dv);
+  }
+  // queries that see a softmax thread's key: [key, key + W] inside its sequence
+  int q_vis_hi = -1;
+  if (warp >= 2 && warp < 10) {
+    const int r = (warp & 3) * 32 + lane, key = k0 + r;
+    if (key < n_rows) {
+      q_vis_hi = packed_seq(cu, n_seq, key, n_rows).y - 1;
+      if (window >= 0) q_vis_hi = min(q_vis_hi, key + min(window, total));
+    }
+    if (r == 0) s_vis[0] = q_vis_hi;
+    if (key == min(k0 + AB2_BK, n_rows) - 1) s_vis[1] = q_vis_hi;
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int q_first = s_vis[0];
+  const int qt_lo = k0 / AB2_BQ;
+  const int nq = s_vis[1] / AB2_BQ - qt_lo + 1;
+  const int steps = G * nq;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      mbar_arrive_expect_tx(kv_full, 2 * AB2_KV_TILE);
+      tma_load_2d(sK, &tm_k, kv_full, kvh * 128, k0);
+      tma_load_2d(sK + 16384, &tm_k, kv_full, kvh * 128 + 64, k0);
+      tma_load_2d(sV, &tm_v, kv_full, kvh * 128, k0);
+      tma_load_2d(sV + 16384, &tm_v, kv_full, kvh * 128 + 64, k0);
+    }
+    bool ok = true;
+    for (int i = 0; i < steps && ok; ++i) {
+      const int st = i % AB2_STAGES;
+      const int hh = kvh * G + i / nq;
+      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      ok = mbar_wait_warp(&qdo_empty[st], ((i / AB2_STAGES) & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_PRODUCER);
+      if (!ok) break;
+      // the tile loads go out first; LSE and D (plain loads, guarded at the
+      // sequence end) overlap them and complete the stage with a second arrival
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&qdo_full[st], 2 * AB2_Q_TILE);
+        uint8_t* q = sQ + st * AB2_Q_TILE;
+        uint8_t* d = sDO + st * AB2_Q_TILE;
+        tma_load_2d(q, &tm_q, &qdo_full[st], hh * 128, q0);
+        tma_load_2d(q + 8192, &tm_q, &qdo_full[st], hh * 128 + 64, q0);
+        tma_load_2d(d, &tm_do, &qdo_full[st], hh * 128, q0);
+        tma_load_2d(d + 8192, &tm_do, &qdo_full[st], hh * 128 + 64, q0);
+      }
+      float* ld = sLD + st * 128;
+      for (int e = lane; e < 64; e += 32) {
+        const int t = q0 + e;
+        const long long li = (long long)hh * total + t;
+        ld[e] = (t < n_rows) ? lse[li] * LOG2E : 0.f;
+        ld[64 + e] = (t < n_rows) ? Dd[li] : 0.f;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qdo_full[st]);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t ID_S = make_idesc(128, 64, false, false, false);   // S^T, dP^T
+      constexpr uint32_t ID_G = make_idesc(128, 128, false, true, false);   // dV, dK (A from TMEM)
+      constexpr uint32_t ID_Q = make_idesc(128, 64, true, true, false);     // dQ^T
+      const uint32_t aK = smem_u32(sK), aV = smem_u32(sV), aDS = smem_u32(sDS);
+      bool ok = mbar_wait(kv_full, 0, abort_flag, ERRW_TIMEOUT_MMA);
+      auto grads = [&](int i) -> bool {
+        const int st = i % AB2_STAGES;
+        if (!mbar_wait(p_full, i & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        tc_fence_after();
+        const uint32_t aQ = smem_u32(sQ + st * AB2_Q_TILE), aDO = smem_u32(sDO + st * AB2_Q_TILE);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
+          // A: P^T / dS^T in TMEM (lane = key, 8 columns per 16 queries)
+          // B: dO / Q as MN-major (hd halves 8 KB apart), K step = 16 query rows
+          mma_bf16_ts(tmem + 128, tmem + 448 + k * 8, smem_desc_sw128(aDO + k * 2048, 8192, 1024), ID_G, acc);
+          mma_bf16_ts(tmem + 0, tmem + 480 + k * 8, smem_desc_sw128(aQ + k * 2048, 8192, 1024), ID_G, acc);
+        }
+        if (!mbar_wait(dq_free, (i & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // A = K^T (MN-major over hd, halves 16 KB apart), B = dS (MN-major over queries), K step = 16 keys
+          mma_bf16_ss(tmem + 384, smem_desc_sw128(aK + k * 2048, 16384, 1024),
+                      smem_desc_sw128(aDS + k * 2048, 8192, 1024), ID_Q, k > 0 ? 1u : 0u);
+        }
+        mma_commit(ds_free);
+        mma_commit(&qdo_empty[st]);
+        mma_commit(dq_full);
+        return true;
+      };
+      for (int i = 0; ok && i < steps; ++i) {
+        const int st = i % AB2_STAGES;
+        if (!mbar_wait(&qdo_full[st], (i / AB2_STAGES) & 1, abort_flag, ERRW_TIMEOUT_MMA)) { ok = false; break; }
+        if (!mbar_wait(s_empty, (i & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_MMA)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t aQ = smem_u32(sQ + st * AB2_Q_TILE), aDO = smem_u32(sDO + st * AB2_Q_TILE);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          // K-major over hd: A rows = keys (halves 16 KB apart), B rows = queries (halves 8 KB apart)
+          const uint32_t ka = (uint32_t)((k >> 2) * 16384 + (k & 3) * 32), kq = (uint32_t)((k >> 2) * 8192 + (k & 3) * 32);
+          mma_bf16_ss(tmem + 256, smem_desc_sw128(aK + ka, 16, 1024), smem_desc_sw128(aQ + kq, 16, 1024), ID_S, k > 0);
+          mma_bf16_ss(tmem + 320, smem_desc_sw128(aV + ka, 16, 1024), smem_desc_sw128(aDO + kq, 16, 1024), ID_S, k > 0);
+        }
+        mma_commit(s_full);
+        if (i > 0 && !grads(i - 1)) { ok = false; break; }
+      }
+      if (ok && steps > 0) ok = grads(steps - 1);
+      mma_commit(acc_done);
+      if (*abort_flag) {
+        mma_commit(drain);
+        const unsigned long long t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0))
+          if (globaltimer_ns() - t0 > 100000000ull) { record_error(ERRW_TIMEOUT_DRAIN); break; }
+      }
+    }
+  } else if (warp < 10) {
+    // ---------------------------------------------------- softmax backward
+    const int qw = warp & 3;
+    const int cb = (warp - 2) >> 2;          // queries cb*32 .. cb*32+31 of the tile
+    const int r = qw * 32 + lane;            // key row within the tile
+    const int key = k0 + r;
+    const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
+    const float scale = rsqrtf(128.f);
+    const float sl2 = LOG2E * scale;
+    bool ok = true;
+    for (int i = 0; i < steps && ok; ++i) {
+      const int st = i % AB2_STAGES;
+      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      ok = mbar_wait_warp(s_full, i & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      if (!ok) break;
+      tc_fence_after();
+      const int tq = q0 + cb * 32;  // first query of this warp's columns
+      const bool need_mask = (k0 + AB2_BK - 1 > tq) || (tq + 31 > q_first) || (k0 + AB2_BK > n_rows);
+      const float4* l2v = reinterpret_cast<const float4*>(sLD + st * 128 + cb * 32);
+      const float4* ddv = reinterpret_cast<const float4*>(sLD + st * 128 + 64 + cb * 32);
+      // P^T and dS^T for this warp's 32 queries, packed to bf16 pairs (query
+      // 2j in the low half); S^T and dP^T come in with one TMEM round trip
+      uint32_t pu[16], du[16];
+      {
+        uint32_t sv[32], dvv[32];
+        tmem_ld_32x32b_x32(lane_addr + 256 + cb * 32, sv);
+        tmem_ld_32x32b_x32(lane_addr + 320 + cb * 32, dvv);
+        tmem_ld_wait();
+        // S^T / dP^T are in registers: the next step's products may overwrite them
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          const float4 a = l2v[g], d = ddv[g];
+          const float l2[4] = {a.x, a.y, a.z, a.w}, dd[4] = {d.x, d.y, d.z, d.w};
+          float pe[4], de[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int t = tq + g * 4 + e;
+            const bool vis = !need_mask || (t >= key && t <= q_vis_hi);
+            pe[e] = vis ? fast_exp2(fmaf(__uint_as_float(sv[g * 4 + e]), sl2, -l2[e])) : 0.f;
+            de[e] = vis ? pe[e] * (__uint_as_float(dvv[g * 4 + e]) - dd[e]) * scale : 0.f;
+          }
+          pu[g * 2] = pack_bf16(pe[0], pe[1]);
+          pu[g * 2 + 1] = pack_bf16(pe[2], pe[3]);
+          du[g * 2] = pack_bf16(de[0], de[1]);
+          du[g * 2 + 1] = pack_bf16(de[2], de[3]);
+        }
+      }
+      // the previous step's dV/dK/dQ MMAs must be done reading P^T / dS^T
+      if (i > 0) {
+        ok = mbar_wait_warp(ds_free, (i - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+        if (!ok) break;
+        tc_fence_after();
+      }
+      tmem_st_32x32b_x16(lane_addr + 448 + cb * 16, pu);
+      tmem_st_32x32b_x16(lane_addr + 480 + cb * 16, du);
+      // rows behind the last sequence may hold anything (0 * NaN is NaN): the
+      // K rows (read by dQ), Q rows (dK) and dO rows (dV) of this tile that lie
+      // there are zeroed before the products that read them.  S^T and dP^T of
+      // these rows and columns are masked, whatever they were computed from.
+      if (n_rows < total) {
+        if (i == 0 && cb == 0 && key >= n_rows) zero_tile_row(sK, 16384, r);
+        if (cb == 1 && r < AB2_BQ && q0 + r >= n_rows) {
+          zero_tile_row(sQ + st * AB2_Q_TILE, 8192, r);
+          zero_tile_row(sDO + st * AB2_Q_TILE, 8192, r);
+        }
+      }
+      uint8_t* drow = sDS + r * 128;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int cc = cb * 4 + c;  // 16-byte chunk (8 queries) within the 128-byte row
+        *reinterpret_cast<uint4*>(drow + ((cc ^ (r & 7)) << 4)) =
+            make_uint4(du[c * 4], du[c * 4 + 1], du[c * 4 + 2], du[c * 4 + 3]);
+      }
+      tmem_st_wait();
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_full);
+    }
+    // dK, dV rows (bf16) for this CTA's keys, columns cb*64 .. cb*64+63, through
+    // two 32-row x 128-byte swizzled staging tiles per warp in the (now idle) Q/dO ring
+    if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(acc_done, 0, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
+      tc_fence_after();
+      uint8_t* stg = sQ + (warp - 2) * 2 * 4096;
+      const bool whole = k0 + qw * 32 + 32 <= n_rows;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        uint32_t v0[32], v1[32];
+        tmem_ld_32x32b_x32(lane_addr + which * 128 + cb * 64, v0);
+        tmem_ld_32x32b_x32(lane_addr + which * 128 + cb * 64 + 32, v1);
+        tmem_ld_wait();
+        uint8_t* prow = stg + which * 4096 + lane * 128;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {  // 16-byte chunk g: columns 8g .. 8g+7
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c0 = g * 8 + 2 * j;
+            const float lo = __uint_as_float(c0 < 32 ? v0[c0] : v1[c0 - 32]);
+            const float hi = __uint_as_float(c0 + 1 < 32 ? v0[c0 + 1] : v1[c0 + 1 - 32]);
+            w[j] = pack_bf16(lo, hi);
+          }
+          if (whole)
+            *reinterpret_cast<uint4*>(prow + ((g ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          else if (key < n_rows)
+            *reinterpret_cast<uint4*>((which ? dv + (long long)key * lddv : dk + (long long)key * lddk) + kvh * 128 +
+                                      cb * 64 + g * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && whole) {
+        tma_store_2d(&tm_dk, stg, kvh * 128 + cb * 64, k0 + qw * 32);
+        tma_store_2d(&tm_dv, stg + 4096, kvh * 128 + cb * 64, k0 + qw * 32);
+        bulk_commit_group();
+        bulk_wait_read0();  // the staging tiles are read before the CTA ends
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------- dQ epilogue
+    // TMEM gives each thread one hd column of dQ^T (64 queries).  A 4x4
+    // transpose among each group of 4 lanes (two butterfly stages of
+    // shuffles) turns that into 4 consecutive hd values of one query, so one
+    // 16-byte fp32 reduction per thread covers 4 rows x 128 bytes per warp:
+    // a quarter of the reduction instructions of one-float-per-lane.
+    const int qw = warp & 3;
+    const int qh = (warp - 10) >> 2;  // queries qh*32 .. qh*32+31 of the tile
+    const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
+    bool ok = true;
+    for (int i = 0; i < steps; ++i) {
+      const int hh = kvh * G + i / nq;
+      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      ok = ok && mbar_wait_warp(dq_full, i & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      uint32_t v0[32];
+      if (ok) {
+        tc_fence_after();
+        tmem_ld_32x32b_x32(lane_addr + 384 + qh * 32, v0);
+        tmem_ld_wait();
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(dq_free);
+      if (ok) {
+        const int m4 = lane & 3;
+        const bool b1 = (m4 & 2) != 0, b0 = (m4 & 1) != 0;
+        const int nv = n_rows - q0 - qh * 32;  // query rows of this half inside the sequence
+        float* dst = dq + (long long)(q0 + qh * 32 + m4) * lddq + hh * 128 + qw * 32 + (lane & ~3);
+#pragma unroll
+        for (int qb = 0; qb < 8; ++qb) {
+          // a[j]: query 4qb+j at this lane's hd  ->  a[j]: query 4qb+m4 at hd (lane&~3)+j
+          float a[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a[j] = __uint_as_float(v0[qb * 4 + j]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {  // swap the off-diagonal 2x2 blocks (lane bit 1)
+            const float y = __shfl_xor_sync(0xffffffffu, b1 ? a[t] : a[2 + t], 2);
+            if (b1) a[t] = y; else a[2 + t] = y;
+          }
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {  // transpose inside each 2x2 block (lane bit 0)
+            const float y = __shfl_xor_sync(0xffffffffu, b0 ? a[2 * t] : a[2 * t + 1], 1);
+            if (b0) a[2 * t] = y; else a[2 * t + 1] = y;
+          }
+          if (4 * qb + m4 < nv) red_add_v4_f32(dst + (long long)(4 * qb) * lddq, a[0], a[1], a[2], a[3]);
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// before the backward: D = rowsum(dO o) of each (row, head) and the fp32 dQ
+// sums set to 0, one warp per (row, head), 4 columns per lane
+__global__ void __launch_bounds__(256)
+    packed_attn_pre_kernel(const bf16* __restrict__ o, long long ldo, const bf16* __restrict__ dO, long long lddo,
+                           float* __restrict__ D, float* __restrict__ dq, const int32_t* __restrict__ cu, int n_seq,
+                           int total, int H) {
+  const int n_rows = packed_rows(cu, n_seq, total);
+  if (blockIdx.x == 0) packed_check(cu, n_seq, total);
+  const long long nw = (long long)n_rows * H;
+  const int lane = threadIdx.x & 31;
+  for (long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5; w < nw;
+       w += ((long long)gridDim.x * blockDim.x) >> 5) {
+    const long long t = w / H;
+    const int h = (int)(w - t * H);
+    const uint2 a = *reinterpret_cast<const uint2*>(o + t * ldo + h * 128 + lane * 4);
+    const uint2 b = *reinterpret_cast<const uint2*>(dO + t * lddo + h * 128 + lane * 4);
+    const __nv_bfloat162 *ha = reinterpret_cast<const __nv_bfloat162*>(&a), *hb = reinterpret_cast<const __nv_bfloat162*>(&b);
+    float acc = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float2 x = __bfloat1622float2(ha[k]), y = __bfloat1622float2(hb[k]);
+      acc = fmaf(x.x, y.x, fmaf(x.y, y.y, acc));
+    }
+    acc = warp_sum(acc);
+    if (lane == 0) D[(long long)h * total + t] = acc;
+    *reinterpret_cast<float4*>(dq + w * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+// after it: dQ rounded to bf16, 8 columns per thread
+__global__ void __launch_bounds__(256)
+    packed_attn_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long lddq,
+                          const int32_t* __restrict__ cu, int n_seq, int total, int H) {
+  const int n_rows = packed_rows(cu, n_seq, total);
+  const int per_row = H * 16;
+  const long long n = (long long)n_rows * per_row;
+  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
+    const long long t = i / per_row;
+    const int c = (int)(i - t * per_row) * 8;
+    float v[8];
+    load8(acc + i * 8, v);
+    store8(dq + t * lddq + c, v);
+  }
+}
+
+}  // namespace gptb

@@ -23,7 +23,8 @@
  *     ACCUMULATED (+=); the caller zeroes them before the first micro-step,
  *     which makes gradient accumulation free.
  *   - All work is enqueued on `stream`; no call synchronises the host except
- *     gptb_device_error().  Pointers must be 16-byte aligned.
+ *     gptb_device_error().  Pointers must be 16-byte aligned (unless an entry
+ *     point says otherwise).
  *   - Return value: GPTB_OK (0) or a negative GPTB_ERR_* code; nothing is
  *     enqueued when an argument check fails.  No exceptions cross the ABI.
  */
@@ -47,8 +48,8 @@ enum {
   GPTB_ERR_TIMEOUT = -4,     /* a bounded device wait expired (see below)    */
   GPTB_ERR_WORKSPACE = -5,   /* workspace too small                          */
   GPTB_ERR_BAD_INPUT = -6    /* a device-side check found invalid input data
-                                (a target id outside [0, vocab)); reported by
-                                gptb_device_error()                          */
+                                (a target id outside [0, vocab), offsets out of
+                                order); reported by gptb_device_error()      */
 };
 
 enum { GPTB_F32 = 0, GPTB_BF16 = 1, GPTB_FP8_E4M3 = 2 };
@@ -368,6 +369,119 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
                           float* lse, int B, int H, int Hkv, int T_max, int window, void* workspace,
                           size_t workspace_bytes, gptb_stream_t stream);
 
+/* Attention over packed sequences of different lengths (a batch of prompts
+ * read whole, or a training batch of sampled answers): causal, grouped-query
+ * heads (kv head of q head h = h / (H/Hkv)), head size 128, softmax scale
+ * 1/sqrt(128).  The rows of all sequences lie one after the other.
+ *   q, k, v: device bf16, `total` rows of H, Hkv, Hkv heads x 128 columns,
+ *            ldq, ldk, ldv elements from row to row (>= heads*128, multiples
+ *            of 8; the three may be column ranges of one array)
+ *   cu_seqlens: device int32 [n_seq+1], 0 = cu[0] <= cu[1] <= ... <= total:
+ *            sequence s has the rows cu[s] .. cu[s+1]-1 (none: an empty one).
+ *            The lengths stay on the device: a captured call follows them.
+ *   window:  -1 = every earlier row of the sequence; W >= 0: the last W+1
+ *   o:       device bf16, total rows of H*128 columns, row stride ldo
+ *   lse:     device fp32 [H, total] (natural log of the softmax denominator
+ *            including its max)
+ * Rows from cu[n_seq] on belong to no sequence: whatever they hold reaches no
+ * result, and their outputs are left as they were.  Inside the sequences q, k,
+ * v (and dout) have to be finite: rows share tiles, and a NaN or infinity can
+ * reach the rows of a neighbouring sequence.  Outputs overlap no input.
+ * Offsets that break the order above are reported by gptb_device_error()
+ * (GPTB_ERR_BAD_INPUT); the outputs are then undefined, and nothing outside
+ * the arrays is touched.
+ * Errors: GPTB_ERR_INVALID_ARG (null or misaligned pointers, strides, shapes),
+ * GPTB_ERR_UNSUPPORTED (not an sm_100 device, total > 2^30). */
+int gptb_packed_attention(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
+                          const int32_t* cu_seqlens, void* o, long long ldo, float* lse, int total, int n_seq, int H,
+                          int Hkv, int window, gptb_stream_t stream);
+
+/* Its backward pass: dq, dk, dv (bf16, overwritten, strided like q, k, v) from
+ * dout (the gradient of o) and the o and lse that the forward call wrote.
+ *   workspace: device, gptb_packed_attention_workspace_bytes(total, H) bytes,
+ *            16-byte aligned
+ * dq is summed over key tiles by fp32 reductions whose order varies, so its
+ * last bit may differ from run to run; dk and dv do not vary. */
+size_t gptb_packed_attention_workspace_bytes(int total, int H);
+int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, long long ldk, const void* v,
+                                   long long ldv, const void* o, long long ldo, const void* dout, long long lddo,
+                                   const float* lse, const int32_t* cu_seqlens, void* dq, long long lddq, void* dk,
+                                   long long lddk, void* dv, long long lddv, int total, int n_seq, int H, int Hkv,
+                                   int window, void* workspace, size_t workspace_bytes, gptb_stream_t stream);
+
+/* One decode step of a batch whose sequences share prompts (several samples of
+ * each prompt): attention of each sequence's newest token over the prompt of
+ * its group, whose keys and values are kept and read once for the group, and
+ * over its own cache.
+ *   q:       device bf16 [B, H, 128]
+ *   k_prefix, v_prefix: device bf16, total_prefix rows of Hkv heads x 128
+ *            columns, ld_prefix elements from row to row: the packed prompts
+ *            (the k and v of gptb_packed_attention serve as they are);
+ *            NULL when total_prefix or n_groups is 0
+ *   cu_prefix: device int32 [n_groups+1]: prompt g has the rows cu_prefix[g] ..
+ *            cu_prefix[g+1]-1
+ *   cu_group: device int32 [n_groups+1]: its samples are the sequences
+ *            cu_group[g] .. cu_group[g+1]-1; one outside every group has no
+ *            prefix.  Both arrays start at 0 and do not decrease.
+ *   k_cache, v_cache: device bf16 [B, T_max, Hkv, 128]: each sequence's own
+ *            tokens, the new one's k and v included
+ *   lens:    device int32 [B], own tokens, 0..T_max; outside of that o = 0 and
+ *            lse = -inf, as for a sequence that sees no key at all
+ *   window:  -1 = all; W >= 0: the last W+1 positions, the prompt's included
+ *            (the new token stands at position plen + lens[b] - 1)
+ *   o:       device bf16 [B, H, 128]; lse: device fp32 [B, H] or NULL
+ *   workspace: device, gptb_prefix_decode_workspace_bytes(B, H, Hkv) bytes,
+ *            16-byte aligned; concurrent calls need one each
+ * Cache rows from lens[b] on and prefix rows of other groups reach no result,
+ * whatever they hold.  Results do not vary from run to run.
+ * Errors as for gptb_packed_attention; GPTB_ERR_WORKSPACE (too small),
+ * GPTB_ERR_UNSUPPORTED (more than 128 query heads per kv head). */
+size_t gptb_prefix_decode_workspace_bytes(int B, int H, int Hkv);
+int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void* v_prefix, long long ld_prefix,
+                                 const int32_t* cu_prefix, int total_prefix, const int32_t* cu_group, int n_groups,
+                                 const void* k_cache, const void* v_cache, const int32_t* lens, int T_max, void* o,
+                                 float* lse, int B, int H, int Hkv, int window, void* workspace,
+                                 size_t workspace_bytes, gptb_stream_t stream);
+
+/* Clipped policy loss with a KL term, from the logits of sampled tokens, with
+ * its gradient.  Per row i (token a, weight w, advantage A):
+ *   lp = z_a - logsumexp(z),  r = exp(lp - logp_old),  d = logp_ref - lp
+ *   loss = sum_i w ( -min(r A, clip(r, 1-clip_lo, 1+clip_hi) A)
+ *                    + beta (exp d - d - 1) )
+ * and dlogits = d loss / d logits (a clipped row keeps its KL term only).
+ *   logits:  device, `rows` rows of `vocab` elements (GPTB_BF16 or GPTB_F32),
+ *            ld elements from row to row; any alignment of an element (16-byte
+ *            aligned rows are the fastest)
+ *   actions: device int32 [rows]; one outside [0, vocab) is reported by
+ *            gptb_device_error() (GPTB_ERR_BAD_INPUT), its row counts as
+ *            weight 0
+ *   weights, advantages, logp_old: device fp32 [rows]; the weights carry the
+ *            normalisation (1/tokens, say).  A row of weight 0 (a prompt token,
+ *            padding) is not read: it adds nothing, logp 0 and a zero gradient
+ *   logp_ref: device fp32 [rows], or NULL (then beta has to be 0)
+ *   dlogits: device, same type, row stride ldd, overwritten; may be the logits
+ *            themselves (ldd = ld then); NULL: no gradient
+ *   logp:    device fp32 [rows]: lp
+ *   stats:   device fp32 [3], overwritten: the loss, sum w (exp d - d - 1) and
+ *            sum of w over the clipped rows (those without policy gradient)
+ *   workspace: device, gptb_policy_loss_workspace_bytes(rows) bytes, 16-byte
+ *            aligned
+ * The only entry points that take pointers of less than 16-byte alignment
+ * (logits, dlogits and the per-row arrays).  Results do not vary from run to
+ * run.  Errors: GPTB_ERR_INVALID_ARG, GPTB_ERR_UNSUPPORTED (dtype),
+ * GPTB_ERR_WORKSPACE. */
+size_t gptb_policy_loss_workspace_bytes(int rows);
+int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
+                     const float* weights, const float* advantages, const float* logp_old, const float* logp_ref,
+                     float clip_lo, float clip_hi, float beta, void* dlogits, long long ldd, float* logp, float* stats,
+                     void* workspace, size_t workspace_bytes, gptb_stream_t stream);
+
+/* logp[i] = logits[i, tokens[i]] - logsumexp(logits[i]): the log-probabilities
+ * that gptb_policy_loss takes as logp_old and logp_ref.  Arguments as there; a
+ * token outside [0, vocab) is reported and gives 0. */
+int gptb_token_logprobs(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* tokens,
+                        float* logp, gptb_stream_t stream);
+
 /* Element casts for data-parallel gradient buckets (bf16 on the wire):
  * y[i] = bf16(x[i] * scale) and y[i] = float(x[i]) * scale, n elements,
  * device pointers, round to nearest-even.  GPTB_ERR_INVALID_ARG for null
@@ -378,8 +492,8 @@ int gptb_cast_bf16_f32(const void* x, float* y, long long n, float scale, gptb_s
 /* Synchronises `stream`, then reads and clears the device error word.
  * Returns GPTB_OK, GPTB_ERR_TIMEOUT if a bounded wait inside a kernel expired
  * (the kernel recorded it, drained and returned), GPTB_ERR_BAD_INPUT if a
- * kernel found invalid input data (a cross-entropy target outside
- * [0, vocab)), or GPTB_ERR_CUDA. */
+ * kernel found invalid input data (a cross-entropy target or an action outside
+ * [0, vocab), sequence offsets out of order), or GPTB_ERR_CUDA. */
 int gptb_device_error(gptb_stream_t stream);
 
 /* Self-test of the bounded waits: sets the wait limit to limit_ns, launches

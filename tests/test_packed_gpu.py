@@ -1,0 +1,160 @@
+"""Packed attention (forward, backward) through the C ABI against the fp64
+oracle.  Every element of o, dq, dk, dv is held to the bound that rounding P and
+dS to bf16, o before D and the result can cause (oracle/rollout.py), with 2 % and
+1e-5 of the largest value for the fp32 arithmetic in between; lse to 1e-4 (128
+products of up to 11.4 in sum, each step of the sum off by at most 2^-24 of it:
+at most 9e-5)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import rollout as orl
+from rollout_inputs import heads, packed, qkv_views
+
+pytestmark = pytest.mark.gpu
+
+LENS = {
+    "one token": [1],
+    "short": [3, 1, 60, 2, 5],
+    "a tile": [128],
+    "a tile and one": [129],
+    "tile edges": [127, 1, 128, 64, 65, 63],
+    "empty ones": [0, 5, 0, 0, 300, 0],
+    "ragged": [700, 13, 257, 40],
+    "many": [1 + i % 7 for i in range(150)],
+}
+
+
+def within(got, want, err):
+    slack = 1.02 * err + 1e-5 * max(1e-30, float(np.abs(want).max(initial=0.0)))
+    off = np.abs(got - want) - slack
+    assert np.all(np.isfinite(got))
+    assert off.size == 0 or off.max() <= 0, (float(np.abs(got - want).max()), float((np.abs(got - want) / slack).max()))
+
+
+def run(gb, lens, H, Hk, window, backward=True, pad=0, seed=0):
+    qkv, dout, cu = packed(lens, H, Hk, seed, pad)
+    q, k, v = qkv_views(qkv, H, Hk)
+    n = q.shape[0]
+    o = torch.full((n, H * 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, n), 7.0, device="cuda")
+    gb.gptb_packed_attention(q, k, v, cu, o, lse, H, Hk, window)
+    got = {"o": o, "lse": lse}
+    if backward:
+        dqkv = torch.full_like(qkv, 7.0)
+        dq, dk, dv = qkv_views(dqkv, H, Hk)
+        ws = torch.full((gb.gptb_packed_attention_workspace_bytes(n, H),), 255, dtype=torch.uint8, device="cuda")
+        gb.gptb_packed_attention_backward(q, k, v, o, dout, lse, cu, dq, dk, dv, H, Hk, window, ws)
+        got |= {"dq": dq, "dk": dk, "dv": dv}
+    assert gb.gptb_device_error() == 0
+    m = int(sum(lens))
+    want = orl.packed_attention(heads(q[:m], H), heads(k[:m], Hk), heads(v[:m], Hk), cu.cpu().numpy(), window,
+                                heads(dout[:m], H) if backward else None)
+    return got, want, m
+
+
+def check(got, want, m, H, Hk):
+    for n in got:
+        if n == "lse":
+            assert np.abs(got[n].double().cpu().numpy()[:, :m] - want[n]).max(initial=0.0) <= 1e-4
+            assert torch.all(got[n][:, m:] == 7.0)
+        else:
+            within(heads(got[n][:m], Hk if n in ("dk", "dv") else H), want[n], want["err"][n])
+            assert torch.all(got[n][m:] == 7.0), n  # rows behind the last sequence are left as they were
+
+
+@pytest.mark.parametrize("name", sorted(LENS))
+@pytest.mark.parametrize("window", [-1, 0, 37])
+def test_packed_attention(cuda_lib, name, window):
+    got, want, m = run(cuda_lib, LENS[name], 4, 2, window)
+    check(got, want, m, 4, 2)
+
+
+@pytest.mark.parametrize("H,Hk", [(1, 1), (6, 6), (10, 5), (8, 1)])
+def test_packed_head_layouts(cuda_lib, H, Hk):
+    got, want, m = run(cuda_lib, [200, 31, 90], H, Hk, -1)
+    check(got, want, m, H, Hk)
+
+
+@pytest.mark.parametrize("pad", [1, 40, 300])
+@pytest.mark.parametrize("lens", [[5], [100, 20], [256], [130, 126]])
+def test_rows_behind_the_last_sequence_hold_nan_and_stay(cuda_lib, lens, pad):
+    got, want, m = run(cuda_lib, lens, 2, 1, -1, pad=pad)
+    check(got, want, m, 2, 1)
+
+
+def test_packed_long_sequence_with_window(cuda_lib):
+    got, want, m = run(cuda_lib, [1500, 900], 2, 2, 300)
+    check(got, want, m, 2, 2)
+
+
+def test_packed_nothing_to_do(cuda_lib):
+    for lens, pad in (([], 0), ([], 9), ([0, 0], 9), ([0], 0)):
+        got, want, m = run(cuda_lib, lens, 2, 1, -1, pad=pad)
+        check(got, want, m, 2, 1)
+
+
+def test_packed_rows_do_not_depend_on_their_neighbours(cuda_lib):
+    """A sequence gives the same rows alone and among others at the same place in its tiles (forward, dk and dv)."""
+    gb = cuda_lib
+    qkv, dout, cu = packed([256, 200, 300], 2, 1, seed=5)
+    alone = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    outs = []
+    for x, d, c, at in ((qkv, dout, cu, 256), (qkv[256:456], dout[256:456], alone, 0)):
+        q, k, v = qkv_views(x, 2, 1)
+        o, lse = torch.empty(len(x), 256, dtype=torch.bfloat16, device="cuda"), torch.empty(2, len(x), device="cuda")
+        gb.gptb_packed_attention(q, k, v, c, o, lse, 2, 1)
+        dqkv = torch.empty(len(x), 512, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(gb.gptb_packed_attention_workspace_bytes(len(x), 2), dtype=torch.uint8, device="cuda")
+        gb.gptb_packed_attention_backward(q, k, v, o, d, lse, c, *qkv_views(dqkv, 2, 1), 2, 1, -1, ws)
+        outs.append((o[at:at + 200], lse[:, at:at + 200], dqkv[at:at + 200, 256:]))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_packed_captured_call_follows_its_lengths(cuda_lib):
+    """A captured forward and backward, replayed with other lengths in the same offsets array, on a stream of its own."""
+    gb = cuda_lib
+    H, Hk, n = 4, 2, 500
+    qkv, dout, _ = packed([n], H, Hk, seed=8)
+    q, k, v = qkv_views(qkv, H, Hk)
+    cu = torch.tensor([0, 100, 500, 500], dtype=torch.int32, device="cuda")
+    o, lse = torch.empty(n, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, n, device="cuda")
+    dqkv = torch.empty_like(qkv)
+    ws = torch.empty(gb.gptb_packed_attention_workspace_bytes(n, H), dtype=torch.uint8, device="cuda")
+
+    def step():
+        gb.gptb_packed_attention(q, k, v, cu, o, lse, H, Hk)
+        gb.gptb_packed_attention_backward(q, k, v, o, dout, lse, cu, *qkv_views(dqkv, H, Hk), H, Hk, -1, ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for new in ([0, 100, 500, 500], [0, 0, 129, 500], [0, 7, 8, 300]):
+        cu.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        m = new[-1]
+        want = orl.packed_attention(heads(q[:m], H), heads(k[:m], Hk), heads(v[:m], Hk), new, -1, heads(dout[:m], H))
+        got = dict(zip(("dq", "dk", "dv"), qkv_views(dqkv, H, Hk)), o=o)
+        for name, t in got.items():
+            within(heads(t[:m], Hk if name in ("dk", "dv") else H), want[name], want["err"][name])
+
+
+def test_bad_offsets_are_reported(cuda_lib):
+    gb = cuda_lib
+    qkv, dout, _ = packed([300], 2, 1)
+    q, k, v = qkv_views(qkv, 2, 1)
+    ws = torch.empty(gb.gptb_packed_attention_workspace_bytes(300, 2), dtype=torch.uint8, device="cuda")
+    for bad in ([0, 200, 100, 300], [0, 400], [3, 300], [0, -5, 300], [0, 2 ** 31 - 1, 300], [0, 300, -2 ** 31]):
+        cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        o, lse = torch.empty(300, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 300, device="cuda")
+        gb.gptb_packed_attention(q, k, v, cu, o, lse, 2, 1)
+        assert gb.gptb_device_error() == gb.ERR_BAD_INPUT, bad
+        gb.gptb_packed_attention_backward(q, k, v, o, dout, lse, cu, *qkv_views(torch.empty_like(qkv), 2, 1), 2, 1, -1, ws)
+        assert gb.gptb_device_error() == gb.ERR_BAD_INPUT, bad
