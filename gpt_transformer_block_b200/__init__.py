@@ -9,6 +9,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgptblock.so")
 MAX_LAYERS = 64
@@ -392,56 +394,67 @@ def gptb_decode_attention(q, k_cache, v_cache, lens, o, lse, B, H, Hkv, T_max, w
                                         _stream(stream)), "gptb_decode_attention")
 
 
-def _rows(name: str, t, cols: int, dtype, device, rows=None):
-    """t as a [rows, >= cols] device matrix with contiguous rows: (address, row stride)."""
-    if t.dim() != 2 or t.shape[1] < cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted [{'rows' if rows is None else rows}, {cols}]")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+# The checks below run at every call of the operators that take tensors as they
+# are: each asks a tensor for as little as it can (a few tenths of a microsecond
+# apiece, next to kernels of ten).
+
+def _device(name: str, t):
+    """t's device, a GPU."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: a tensor of device memory is wanted, not on {dev}")
+    return dev
+
+
+def _rows(name: str, t, cols: int, dtype, device, rows):
+    """t as a [rows, >= cols] matrix whose rows are contiguous: (address, row stride)."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
+        raise ValueError(f"{name}: shape {tuple(shape)}, wanted [{rows}, {cols}]")
+    if stride[1] != 1 and shape[1] > 1:
         raise ValueError(f"{name}: its rows have to be contiguous")
-    _like(name, t, dtype, device)
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {dtype} on {device}")
     # (one row has no stride to speak of)
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _like(name: str, t, dtype, device):
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: {t.dtype}, wanted {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: a tensor of device memory is wanted, not on {t.device}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, wanted {device}")
+    return t.data_ptr(), stride[0] if rows > 1 else max(stride[0], shape[1])
 
 
 def _flat(name: str, t, dtype, device, count: int):
-    """t as a contiguous device array of count elements: its address."""
-    _like(name, t, dtype, device)
+    """t as a contiguous array of count elements: its address."""
     if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted {count} contiguous elements")
+    if t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: {t.dtype} on {t.device}, wanted {dtype} on {device}")
     return t.data_ptr()
 
 
 def _workspace(t, device):
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
+    if t.device != device or not t.is_contiguous():
         raise ValueError(f"workspace: contiguous memory of {device} is wanted")
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+# the current stream's handle without a Stream object around it (3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _enqueue(device, fn, args, stream, what: str):
     """fn(*args, stream) with the tensors' device as the current one; stream: that device's current one by default."""
-    import torch
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, _stream(stream)), what)
-    with torch.cuda.device(device):
-        _check(fn(*args, _stream(stream)), what)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _enqueue(device, fn, args, stream, what)
+    rc = fn(*args, _raw_stream(device.index) if stream is None else _stream(stream))
+    if rc != OK:
+        raise GPTBError(rc, what)
 
 
 def gptb_packed_attention(q, k, v, cu_seqlens, o, lse, H, Hkv, window=-1, stream=None):
     """Causal attention over packed sequences: q, o [total, H*128], k, v [total, Hkv*128] bf16 (column ranges of a
     wider array are fine), cu_seqlens int32 [n_seq+1], lse fp32 [H, total]; all on one device."""
-    import torch
-    bf, dev, H, Hkv = torch.bfloat16, q.device, int(H), int(Hkv)
+    bf, dev, H, Hkv = torch.bfloat16, _device("q", q), int(H), int(Hkv)
     n = q.shape[0]
-    args = (*_rows("q", q, H * 128, bf, dev), *_rows("k", k, Hkv * 128, bf, dev, n),
+    args = (*_rows("q", q, H * 128, bf, dev, n), *_rows("k", k, Hkv * 128, bf, dev, n),
             *_rows("v", v, Hkv * 128, bf, dev, n), _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
             *_rows("o", o, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n), n,
             cu_seqlens.numel() - 1, H, Hkv, int(window))
@@ -455,10 +468,9 @@ def gptb_packed_attention_workspace_bytes(total: int, H: int) -> int:
 def gptb_packed_attention_backward(q, k, v, o, dout, lse, cu_seqlens, dq, dk, dv, H, Hkv, window, workspace,
                                    stream=None):
     """Gradients dq, dk, dv (bf16, overwritten) of gptb_packed_attention from dout and its o and lse."""
-    import torch
-    bf, dev, H, Hkv = torch.bfloat16, q.device, int(H), int(Hkv)
+    bf, dev, H, Hkv = torch.bfloat16, _device("q", q), int(H), int(Hkv)
     n = q.shape[0]
-    args = (*_rows("q", q, H * 128, bf, dev), *_rows("k", k, Hkv * 128, bf, dev, n),
+    args = (*_rows("q", q, H * 128, bf, dev, n), *_rows("k", k, Hkv * 128, bf, dev, n),
             *_rows("v", v, Hkv * 128, bf, dev, n), *_rows("o", o, H * 128, bf, dev, n),
             *_rows("dout", dout, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n),
             _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
@@ -477,17 +489,15 @@ def gptb_prefix_decode_attention(q, k_prefix, v_prefix, cu_prefix, cu_group, k_c
     """One decode step of sequences that share prompts: q, o [B, H, 128], k_prefix, v_prefix [rows, Hkv*128] (packed
     prompts; a common row stride), cu_prefix, cu_group int32 [n_groups+1], k_cache, v_cache [B, T_max, Hkv, 128], lens
     int32 [B], lse fp32 [B, H] or None."""
-    import torch
-    bf, i32, dev, H, Hkv = torch.bfloat16, torch.int32, q.device, int(H), int(Hkv)
-    B, T = k_cache.shape[0], k_cache.shape[1]
-    kp, ld = _rows("k_prefix", k_prefix, Hkv * 128, bf, dev)
-    vp, ldv = _rows("v_prefix", v_prefix, Hkv * 128, bf, dev, k_prefix.shape[0])
-    if ld != ldv and k_prefix.shape[0] > 1:
+    bf, i32, dev, H, Hkv = torch.bfloat16, torch.int32, _device("q", q), int(H), int(Hkv)
+    B, T = k_cache.shape[:2]
+    P, n = k_prefix.shape[0], cu_prefix.numel()
+    kp, ld = _rows("k_prefix", k_prefix, Hkv * 128, bf, dev, P)
+    vp, ldv = _rows("v_prefix", v_prefix, Hkv * 128, bf, dev, P)
+    if ld != ldv and P > 1:
         raise ValueError("k_prefix and v_prefix have to have the same row stride")
-    if cu_prefix.numel() != cu_group.numel():
-        raise ValueError("cu_prefix and cu_group have to have the same length")
-    args = (_flat("q", q, bf, dev, B * H * 128), kp, vp, max(ld, ldv), _flat("cu_prefix", cu_prefix, i32, dev, cu_prefix.numel()),
-            k_prefix.shape[0], _flat("cu_group", cu_group, i32, dev, cu_prefix.numel()), max(0, cu_prefix.numel() - 1),
+    args = (_flat("q", q, bf, dev, B * H * 128), kp, vp, max(ld, ldv), _flat("cu_prefix", cu_prefix, i32, dev, n), P,
+            _flat("cu_group", cu_group, i32, dev, n), max(0, n - 1),
             _flat("k_cache", k_cache, bf, dev, B * T * Hkv * 128), _flat("v_cache", v_cache, bf, dev, B * T * Hkv * 128),
             _flat("lens", lens, i32, dev, B), T, _flat("o", o, bf, dev, B * H * 128),
             None if lse is None else _flat("lse", lse, torch.float32, dev, B * H), B, H, Hkv, int(window),
@@ -500,7 +510,6 @@ def gptb_policy_loss_workspace_bytes(rows: int) -> int:
 
 
 def _logits_dtype(t) -> int:
-    import torch
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"logits: {t.dtype}, wanted bfloat16 or float32")
     return BF16 if t.dtype == torch.bfloat16 else F32
@@ -511,10 +520,8 @@ def gptb_policy_loss(logits, actions, weights, advantages, logp_old, logp_ref, c
     """Clipped policy loss with a KL term on logits [rows, vocab] (bf16 or fp32): stats fp32 [3] gets (loss, KL, clipped
     weight), logp fp32 [rows] the tokens' log-probabilities, dlogits (None, another array or the logits themselves) the
     gradient."""
-    import torch
-    f32, dev, (n, V) = torch.float32, logits.device, logits.shape
-    dt = _logits_dtype(logits)
-    z, ld = _rows("logits", logits, V, logits.dtype, dev)
+    f32, dt, dev, (n, V) = torch.float32, _logits_dtype(logits), _device("logits", logits), logits.shape
+    z, ld = _rows("logits", logits, V, logits.dtype, dev, n)
     dz, ldd = (None, 0) if dlogits is None else _rows("dlogits", dlogits, V, logits.dtype, dev, n)
     args = (z, ld, dt, n, V, _flat("actions", actions, torch.int32, dev, n), _flat("weights", weights, f32, dev, n),
             _flat("advantages", advantages, f32, dev, n), _flat("logp_old", logp_old, f32, dev, n),
@@ -526,10 +533,8 @@ def gptb_policy_loss(logits, actions, weights, advantages, logp_old, logp_ref, c
 
 def gptb_token_logprobs(logits, tokens, logp, stream=None):
     """logp[i] = log softmax(logits[i])[tokens[i]] of logits [rows, vocab] (bf16 or fp32)."""
-    import torch
-    dev, (n, V) = logits.device, logits.shape
-    dt = _logits_dtype(logits)
-    args = (*_rows("logits", logits, V, logits.dtype, dev), dt, n, V, _flat("tokens", tokens, torch.int32, dev, n),
+    dt, dev, (n, V) = _logits_dtype(logits), _device("logits", logits), logits.shape
+    args = (*_rows("logits", logits, V, logits.dtype, dev, n), dt, n, V, _flat("tokens", tokens, torch.int32, dev, n),
             _flat("logp", logp, torch.float32, dev, n))
     _enqueue(dev, load().gptb_token_logprobs, args, stream, "gptb_token_logprobs")
 

@@ -192,6 +192,23 @@ bool make_tmap_3d(CUtensorMap* m, const void* ptr, bool f32, uint64_t inner, uin
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device
+// (the call costs about as much host time as the launch itself)
+struct SmemOnce {
+  std::atomic<unsigned long long> done{0};
+};
+template <class K>
+int allow_smem(K kernel, int bytes, SmemOnce& once) {
+  int dev = 0;
+  CK(cudaGetDevice(&dev));
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (once.done.load(std::memory_order_relaxed) & bit)) return GPTB_OK;
+  CK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (dev < 64) once.done.fetch_or(bit, std::memory_order_relaxed);
+  return GPTB_OK;
+}
+SmemOnce g_smem_packed_fwd, g_smem_packed_bwd, g_smem_prefix;
+
 // --------------------------------------------------------------- GEMM ----
 struct Op {
   const void* p;
@@ -1527,7 +1544,7 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
   if (!packed_map(&tq, q, H, total, ldq, 128) || !packed_map(&tk, k, Hkv, total, ldk, 128) ||
       !packed_map(&tv, v, Hkv, total, ldv, 128) || !packed_map(&to, o, H, total, ldo, 32))
     return GPTB_ERR_CUDA;
-  CK(cudaFuncSetAttribute(packed_attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FA_SMEM));
+  TRY(allow_smem(packed_attn_fwd_kernel, FA_SMEM, g_smem_packed_fwd));
   packed_attn_fwd_kernel<<<(unsigned)grid, FA_THREADS, FA_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(
       tq, tk, tv, to, static_cast<bf16*>(o), ldo, lse, cu_seqlens, n_seq, total, H, Hkv, window);
   CKL();
@@ -1568,7 +1585,7 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
   packed_attn_pre_kernel<<<blocks((long long)total * H * 32), 256, 0, st>>>(
       static_cast<const bf16*>(o), ldo, static_cast<const bf16*>(dout), lddo, D, acc, cu_seqlens, n_seq, total, H);
   CKL();
-  CK(cudaFuncSetAttribute(packed_attn_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB2_SMEM));
+  TRY(allow_smem(packed_attn_bwd_kernel, AB2_SMEM, g_smem_packed_bwd));
   packed_attn_bwd_kernel<<<(unsigned)grid, AB2_THREADS, AB2_SMEM, st>>>(
       tq, tk, tv, tdo, tdk, tdv, static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, lse, D, acc, cu_seqlens,
       n_seq, total, H, Hkv, window);
@@ -1668,7 +1685,7 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
                  !packed_map(&tvp, v_prefix, Hkv, total_prefix, ld_prefix, PD_BOX)))
     return GPTB_ERR_CUDA;
   const int grid = (int)std::max(1ll, std::min<long long>(tiles, std::min(dev_info().sms, PD_MAX_CTAS)));
-  CK(cudaFuncSetAttribute(prefix_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, PD_SMEM));
+  TRY(allow_smem(prefix_split_kernel, PD_SMEM, g_smem_prefix));
   prefix_split_kernel<<<grid, PD_THREADS, PD_SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, a);
   CKL();
   prefix_combine_kernel<<<(unsigned)(((long long)B * H + 3) / 4), 128, 0, st>>>(a, static_cast<bf16*>(o), lse, grid);
@@ -1682,25 +1699,35 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
 
 namespace {
 
-// CTAs of the row kernel: two to an SM
-int policy_ctas(int rows) { return std::max(1, std::min(rows, std::min(512, std::max(1, dev_info().sms) * 2))); }
+constexpr int POL_MAX_CTAS = 512;  // (partial sums in the workspace)
+SmemOnce g_smem_policy[2];
 
 template <class T>
-int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, cudaStream_t st) {
-  constexpr int VEC = 16 / (int)sizeof(T);
-  const bool vec = aligned16(logits) && a.ld % VEC == 0 && (!dlogits || (aligned16(dlogits) && a.ldd % VEC == 0));
-  const int grid = policy_ctas(a.rows);
-  if (vec)
-    policy_rows_kernel<T, VEC><<<grid, POL_THREADS, 0, st>>>(static_cast<const T*>(logits), static_cast<T*>(dlogits), a);
-  else
-    policy_rows_kernel<T, 1><<<grid, POL_THREADS, 0, st>>>(static_cast<const T*>(logits), static_cast<T*>(dlogits), a);
+bool policy_aligned(const void* logits, const void* dlogits, const PolicyArgs& a) {
+  constexpr int N = 16 / (int)sizeof(T);
+  return aligned16(logits) && a.ld % N == 0 && (!dlogits || (aligned16(dlogits) && a.ldd % N == 0));
+}
+
+// the row kernel, `*ctas` CTAs of it: as many as the SMs hold
+template <class T>
+int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, int* ctas, cudaStream_t st) {
+  const T* z = static_cast<const T*>(logits);
+  T* dz = static_cast<T*>(dlogits);
+  const bool aligned = policy_aligned<T>(logits, dlogits, a);
+  *ctas = std::max(1, std::min(a.rows, std::min(POL_MAX_CTAS, std::max(1, dev_info().sms) * (aligned ? 3 : 2))));
+  if (aligned) {
+    TRY(allow_smem(policy_rows_kernel<T, true>, POL_SMEM, g_smem_policy[sizeof(T) == 2]));
+    policy_rows_kernel<T, true><<<*ctas, POL_THREADS, POL_SMEM, st>>>(z, dz, a);
+  } else {
+    policy_rows_kernel<T, false><<<*ctas, POL_THREADS, 0, st>>>(z, dz, a);
+  }
   CKL();
   return GPTB_OK;
 }
 bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int policy_shape(const void* logits, long long ld, int dtype, int rows, int vocab) {
   if (dtype != GPTB_F32 && dtype != GPTB_BF16) return GPTB_ERR_UNSUPPORTED;
-  if (rows < 0 || vocab < 1 || vocab > (1 << 30) || ld < vocab || ld >= (1ll << 36)) return GPTB_ERR_INVALID_ARG;
+  if (rows < 0 || rows > (1 << 29) || vocab < 1 || vocab > (1 << 30) || ld < vocab || ld >= (1ll << 36)) return GPTB_ERR_INVALID_ARG;
   // (empty arrays may have no address)
   if (rows > 0 && (!logits || !aligned_to(logits, dtype == GPTB_F32 ? 4 : 2))) return GPTB_ERR_INVALID_ARG;
   return GPTB_OK;
@@ -1712,7 +1739,7 @@ extern "C" {
 
 size_t gptb_policy_loss_workspace_bytes(int rows) {
   if (rows < 0) return 0;
-  return (size_t)std::min(rows, 512) * 3 * sizeof(double) + 256;
+  return (size_t)std::min(rows, POL_MAX_CTAS) * 3 * sizeof(double) + 256;
 }
 
 int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
@@ -1736,8 +1763,10 @@ int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int 
   }
   PolicyArgs a{actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, logp,
                static_cast<double*>(workspace), ld, ldd, rows, vocab};
-  TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, st) : policy_launch<bf16>(logits, dlogits, a, st));
-  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, policy_ctas(rows), stats);
+  int ctas = 0;
+  TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, &ctas, st)
+                        : policy_launch<bf16>(logits, dlogits, a, &ctas, st));
+  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, ctas, stats);
   CKL();
   return GPTB_OK;
 }
@@ -1749,7 +1778,9 @@ int gptb_token_logprobs(const void* logits, long long ld, int dtype, int rows, i
   if (!tokens || !logp) return GPTB_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PolicyArgs a{tokens, nullptr, nullptr, nullptr, nullptr, 0.f, 0.f, 0.f, logp, nullptr, ld, 0, rows, vocab};
-  return dtype == GPTB_F32 ? policy_launch<float>(logits, nullptr, a, st) : policy_launch<bf16>(logits, nullptr, a, st);
+  int ctas = 0;
+  return dtype == GPTB_F32 ? policy_launch<float>(logits, nullptr, a, &ctas, st)
+                           : policy_launch<bf16>(logits, nullptr, a, &ctas, st);
 }
 
 int gptb_cast_f32_bf16(const float* x, void* y, long long n, float scale, gptb_stream_t stream) {

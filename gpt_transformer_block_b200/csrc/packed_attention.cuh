@@ -204,13 +204,17 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
         return true;
       };
       if (ok && in(0, jlo)) ok = issue_s(0, jlo);
-      if (ok && hi[1] >= lo[1]) ok = issue_s(1, lo[1]);
+      if (ok && in(1, jlo)) ok = issue_s(1, jlo);
       for (int j = jlo; ok && j <= jhi; ++j) {
         if (in(0, j)) {
           ok = issue_pv(0, j) && (j + 1 > hi[0] || issue_s(0, j + 1));
           if (!ok) break;
         }
-        if (in(1, j)) ok = issue_pv(1, j) && (j + 1 > hi[1] || issue_s(1, j + 1));
+        // (the second query tile may begin many key tiles after the first: a
+        // sequence that ends between them.  Its first S waits for its turn, as
+        // the K ring holds two tiles.)
+        if (in(1, j) && !issue_pv(1, j)) break;
+        if (in(1, j + 1)) ok = issue_s(1, j + 1);
       }
       if (*abort_flag) {
         mma_commit(drain);

@@ -21,6 +21,7 @@ LENS = {
     "tile edges": [127, 1, 128, 64, 65, 63],
     "empty ones": [0, 5, 0, 0, 300, 0],
     "ragged": [700, 13, 257, 40],
+    "ends between the tiles of a pair": [640, 300, 212, 500],
     "many": [1 + i % 7 for i in range(150)],
 }
 
@@ -86,6 +87,14 @@ def test_rows_behind_the_last_sequence_hold_nan_and_stay(cuda_lib, lens, pad):
 def test_packed_long_sequence_with_window(cuda_lib):
     got, want, m = run(cuda_lib, [1500, 900], 2, 2, 300)
     check(got, want, m, 2, 2)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_packed_random_lengths(cuda_lib, seed):
+    r = np.random.default_rng(seed)
+    lens = np.exp(r.uniform(0, np.log(900), r.integers(3, 12))).astype(int).tolist()
+    got, want, m = run(cuda_lib, lens, 2, 1, [-1, -1, 200][seed % 3], seed=seed, pad=seed % 2 * 31)
+    check(got, want, m, 2, 1)
 
 
 def test_packed_nothing_to_do(cuda_lib):

@@ -88,10 +88,15 @@ def test_gradient_over_the_logits_and_none_at_all(cuda_lib, dtype, V, pad, offse
     gb = cuda_lib
     d = policy_case(8, V, dtype, seed=5, pad=pad, offset=offset)
     dz, logp, stats = check(gb, d)
+    # vectors are cut at the gradient's alignment, so where it lies otherwise than the logits the sums are taken in
+    # another order: each result is within E of the exact one, two of them within 2 E of each other
+    alike = offset == 0
+    same = torch.equal if alike else lambda x, y: bool((x - y).abs().max() <= 2 * E)
     _, lp0, st0 = call(gb, d, out=None)
-    assert torch.equal(lp0, logp) and torch.equal(st0, stats)
-    same, lp1, st1 = call(gb, d, out="same")  # overwrites the logits
-    assert same is d["z"] and torch.equal(same, dz) and torch.equal(lp1, logp) and torch.equal(st1, stats)
+    assert same(lp0, logp) and same(st0, stats)
+    over, lp1, st1 = check(gb, d, out="same")  # overwrites the logits
+    assert over is d["z"] and torch.equal(lp1, lp0) and torch.equal(st1, st0)
+    assert not alike or torch.equal(over, dz)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])

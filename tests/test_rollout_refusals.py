@@ -98,12 +98,22 @@ def test_the_binding_refuses_host_tensors_types_and_shapes(gb):
     cu, lse = torch.zeros(2, dtype=torch.int32), torch.zeros(2, 10)
     with pytest.raises(ValueError, match="device memory"):
         gb.gptb_packed_attention(q, k, k, cu, q, lse, 2, 1)
-    with pytest.raises(ValueError, match="q: torch.float32"):
-        gb.gptb_packed_attention(q.float(), k, k, cu, q, lse, 2, 1)
-    with pytest.raises(ValueError, match="q: shape"):
-        gb.gptb_packed_attention(q, k, k, cu, q, lse, 4, 1)
-    with pytest.raises(ValueError, match="contiguous"):
-        gb.gptb_packed_attention(torch.zeros(256, 10, dtype=BF).t(), k, k, cu, q, lse, 2, 1)
+    # the checks of one argument, on the device that the others are on
+    cpu = q.device
+    assert gb._rows("q", q, 256, BF, cpu, 10) == (q.data_ptr(), 256)
+    assert gb._rows("q", q[:, 128:], 128, BF, cpu, 10) == (q.data_ptr() + 256, 256)
+    assert gb._rows("q", q[3:4, 128:], 128, BF, cpu, 1)[1] >= 128
+    for bad, why in ((q.float(), "float32"), (q[:, :200], "shape"), (q[:9], "shape"), (q[0], "shape"),
+                     (torch.zeros(256, 10, dtype=BF).t(), "contiguous"), (q.to("meta"), "on meta")):
+        with pytest.raises(ValueError, match=why):
+            gb._rows("q", bad, 256, BF, cpu, 10)
+    assert gb._flat("cu", cu, torch.int32, cpu, 2) == cu.data_ptr()
+    for bad, why in ((cu.long(), "int64"), (cu[:1], "shape"), (torch.zeros(4, dtype=torch.int32)[::2], "shape"),
+                     (cu.to("meta"), "on meta")):
+        with pytest.raises(ValueError, match=why):
+            gb._flat("cu", bad, torch.int32, cpu, 2)
+    with pytest.raises(ValueError, match="workspace"):
+        gb._workspace(torch.zeros(8, device="meta"), cpu)
     z = torch.zeros(4, 8, dtype=torch.float16)
     with pytest.raises(ValueError, match="float16"):
         gb.gptb_token_logprobs(z, cu, lse)
