@@ -1699,30 +1699,46 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
 
 namespace {
 
-constexpr int POL_MAX_CTAS = 512;  // (partial sums in the workspace)
-SmemOnce g_smem_policy[2];
+constexpr int POL_MAX_PARTS = 512;  // partial sums in the workspace
+SmemOnce g_smem_policy[4];
 
-template <class T>
-bool policy_aligned(const void* logits, const void* dlogits, const PolicyArgs& a) {
-  constexpr int N = 16 / (int)sizeof(T);
-  return aligned16(logits) && a.ld % N == 0 && (!dlogits || (aligned16(dlogits) && a.ldd % N == 0));
-}
-
-// the row kernel, `*ctas` CTAs of it: as many as the SMs hold
-template <class T>
-int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, int* ctas, cudaStream_t st) {
-  const T* z = static_cast<const T*>(logits);
-  T* dz = static_cast<T*>(dlogits);
-  const bool aligned = policy_aligned<T>(logits, dlogits, a);
-  *ctas = std::max(1, std::min(a.rows, std::min(POL_MAX_CTAS, std::max(1, dev_info().sms) * (aligned ? 3 : 2))));
-  if (aligned) {
-    TRY(allow_smem(policy_rows_kernel<T, true>, POL_SMEM, g_smem_policy[sizeof(T) == 2]));
-    policy_rows_kernel<T, true><<<*ctas, POL_THREADS, POL_SMEM, st>>>(z, dz, a);
-  } else {
-    policy_rows_kernel<T, false><<<*ctas, POL_THREADS, 0, st>>>(z, dz, a);
-  }
+// the row kernel, as many CTAs of it as the SMs hold; *parts: the clusters that leave partial sums
+template <class T, bool ALIGNED>
+int policy_rows(const T* z, T* dz, PolicyArgs a, int* parts, cudaStream_t st) {
+  TRY(allow_smem(policy_rows_kernel<T, ALIGNED>, POL_SMEM, g_smem_policy[(sizeof(T) == 2) * 2 + ALIGNED]));
+  // CTAs per row: two if one does not hold it (2000 fp32 rows of 50257: 235 us,
+  // against 261 with one that takes the rest from L2 and 365 and 417 with three
+  // and four, which hold all but wait for one another); more when there are
+  // fewer rows than CTAs, down to two vectors per thread (29 bf16 rows of
+  // 32768: 8.8 us with 8, 9.7 with one)
+  const long long row = ((long long)a.V * sizeof(T) + 15) / 16, ctas = std::max(1, dev_info().sms) * POL_CTAS;
+  const long long hold = row > POL_KEEP * POL_THREADS ? 2 : 1;
+  const long long fill = std::min(ctas / a.rows, row / (2 * POL_THREADS));
+  a.cs = (int)std::min<long long>(POL_CLUSTER, std::max(hold, fill));
+  *parts = (int)std::max(1ll, std::min<long long>(a.rows, std::min<long long>(POL_MAX_PARTS, ctas / a.cs)));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(*parts * a.cs));
+  cfg.blockDim = dim3(POL_THREADS);
+  cfg.dynamicSmemBytes = POL_SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  CK(cudaLaunchKernelEx(&cfg, policy_rows_kernel<T, ALIGNED>, z, dz, a));
   CKL();
   return GPTB_OK;
+}
+
+template <class T>
+int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, int* parts, cudaStream_t st) {
+  const T* z = static_cast<const T*>(logits);
+  T* dz = static_cast<T*>(dlogits);
+  constexpr int N = 16 / (int)sizeof(T);
+  const bool aligned = aligned16(z) && a.ld % N == 0 && (!dz || (aligned16(dz) && a.ldd % N == 0));
+  return aligned ? policy_rows<T, true>(z, dz, a, parts, st) : policy_rows<T, false>(z, dz, a, parts, st);
 }
 bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int policy_shape(const void* logits, long long ld, int dtype, int rows, int vocab) {
@@ -1739,7 +1755,7 @@ extern "C" {
 
 size_t gptb_policy_loss_workspace_bytes(int rows) {
   if (rows < 0) return 0;
-  return (size_t)std::min(rows, POL_MAX_CTAS) * 3 * sizeof(double) + 256;
+  return (size_t)std::min(rows, POL_MAX_PARTS) * 3 * sizeof(double) + 256;
 }
 
 int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
@@ -1762,11 +1778,11 @@ int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int 
     return GPTB_OK;
   }
   PolicyArgs a{actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, logp,
-               static_cast<double*>(workspace), ld, ldd, rows, vocab};
-  int ctas = 0;
-  TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, &ctas, st)
-                        : policy_launch<bf16>(logits, dlogits, a, &ctas, st));
-  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, ctas, stats);
+               static_cast<double*>(workspace), ld, ldd, rows, vocab, 1};
+  int parts = 0;
+  TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, &parts, st)
+                        : policy_launch<bf16>(logits, dlogits, a, &parts, st));
+  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, parts, stats);
   CKL();
   return GPTB_OK;
 }
@@ -1777,10 +1793,10 @@ int gptb_token_logprobs(const void* logits, long long ld, int dtype, int rows, i
   if (rows == 0) return GPTB_OK;
   if (!tokens || !logp) return GPTB_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  PolicyArgs a{tokens, nullptr, nullptr, nullptr, nullptr, 0.f, 0.f, 0.f, logp, nullptr, ld, 0, rows, vocab};
-  int ctas = 0;
-  return dtype == GPTB_F32 ? policy_launch<float>(logits, nullptr, a, &ctas, st)
-                           : policy_launch<bf16>(logits, nullptr, a, &ctas, st);
+  PolicyArgs a{tokens, nullptr, nullptr, nullptr, nullptr, 0.f, 0.f, 0.f, logp, nullptr, ld, 0, rows, vocab, 1};
+  int parts = 0;
+  return dtype == GPTB_F32 ? policy_launch<float>(logits, nullptr, a, &parts, st)
+                           : policy_launch<bf16>(logits, nullptr, a, &parts, st);
 }
 
 int gptb_cast_f32_bf16(const float* x, void* y, long long n, float scale, gptb_stream_t stream) {

@@ -12,19 +12,21 @@
 // A row of weight 0 carries nothing: its logits are not read, its gradient is 0.
 //
 // Bound by HBM: one read of the rows that count and one write of the gradient.
-// A CTA takes one row at a time and keeps its first 64 KB on the SM between the
-// three steps that need it (maximum, sum of exponentials, gradient); what is
-// longer comes back from L2 for the gradient.  The next row's loads go out as
-// the gradient leaves, so that HBM stays busy through the reductions.  The
-// row's few scalars, loaded a row ahead, are worked out in double by one warp
-// (the ratio is held against the clip borders, and the exponentials of
-// differences lose digits in fp32).
-// Rows that start on 16-byte boundaries stay in shared memory, filled by
-// asynchronous copies: three CTAs per SM.  Other rows stay in registers, two
-// CTAs per SM: vectors of 16 bytes are cut at the gradient's alignment, and
-// where the logits row starts elsewhere each is put together from two
-// neighbouring 16-byte loads (the second is the next lane's first: an L1 hit),
-// so an odd vocabulary streams like an even one.
+// A row is held in shared memory between the three steps that need it (maximum,
+// sum of exponentials, gradient), 66 KB of it by a CTA; what is longer comes back
+// from L2 for the gradient.  A few rows, or long ones, are shared out over the
+// CTAs of a cluster.  The next
+// row's loads go out as the gradient leaves, so that HBM stays busy through the
+// reductions (three CTAs per SM, 8192 bf16 rows of 32768 of which a third do not
+// count: 176 us, 5.1 TB/s; the exponentials, two per element, take about 0.6 of
+// the time on their unit, which the loads have to overlap with).  The row's few scalars, loaded a row ahead, are worked out in
+// double by one warp (the ratio is held against the clip borders, and the
+// exponentials of differences lose digits in fp32).
+// Rows that start on 16-byte boundaries are filled by asynchronous copies.  In
+// other ones vectors of 16 bytes are cut at the gradient's alignment, and where
+// the logits row starts elsewhere each is put together from two neighbouring
+// 16-byte loads (the second is the next lane's first: an L1 hit), so an odd
+// vocabulary streams like an even one.
 #pragma once
 #include <cfloat>
 
@@ -34,18 +36,21 @@ namespace gptb {
 
 constexpr int POL_THREADS = 384;
 constexpr int POL_WARPS = POL_THREADS / 32;
-constexpr int POL_KEEP = 11;  // 16-byte vectors of a row that a thread keeps: 66 KB per CTA
-constexpr int POL_AHEAD = 2; // ... of a long row's rest that it loads at once
-constexpr int POL_SMEM = POL_KEEP * POL_THREADS * 16;
+constexpr int POL_CTAS = 3;    // per SM
+constexpr int POL_KEEP = 11;   // 16-byte vectors of a row that a thread keeps
+constexpr int POL_SMEM = POL_KEEP * POL_THREADS * 16;  // 66 KB
+constexpr int POL_BATCH = 4;   // vectors that a thread has in flight where they pass through registers
+constexpr int POL_CLUSTER = 8; // most CTAs that share a row
 
 struct PolicyArgs {
   const int32_t* actions;
   const float *weights, *adv, *lp_old, *lp_ref;  // weights NULL: log-probabilities only; lp_ref NULL: d = 0
   float clip_lo, clip_hi, beta;
   float* logp;     // [rows]
-  double* part;    // [gridDim.x][3] this CTA's sums of w(-s + beta k), w k, w [clipped]
+  double* part;    // [clusters][3] this cluster's sums of w(-s + beta k), w k, w [clipped]
   long long ld, ldd;
   int rows, V;
+  int cs;  // CTAs per row (cluster size)
 };
 
 // 16 bytes as elements
@@ -161,39 +166,17 @@ __device__ __forceinline__ void policy_in(const PolicyArgs& a, int i, PolicyIn* 
 }
 __device__ __forceinline__ void policy_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// The vectors tid, tid + POL_THREADS, ... of a row that a thread keeps: slots of
-// its own, in shared memory or in registers.
-template <class T, bool ALIGNED>
-struct PolicyKeep;
-template <class T>
-struct PolicyKeep<T, true> {
-  uint32_t at;  // shared-memory address of slot 0
-  __device__ __forceinline__ PolicyKeep(uint8_t* smem) : at(smem_u32(smem) + threadIdx.x * 16) {}
-  __device__ __forceinline__ void fill(int j, const PolicyRowView<T, true>& row, int c) {
-    if (row.whole(c)) {
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at + j * POL_THREADS * 16),
-                   "l"(row.z + (long long)c * PolVec<T>::N) : "memory");
-    } else {
-      const uint4 u = row.load(c);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + j * POL_THREADS * 16), "r"(u.x), "r"(u.y),
-                   "r"(u.z), "r"(u.w) : "memory");
-    }
-  }
-  __device__ __forceinline__ void wait() { policy_wait(); }  // all fills so far have landed
-  __device__ __forceinline__ uint4 get(int j) const {
-    uint4 u;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                 : "r"(at + j * POL_THREADS * 16) : "memory");
-    return u;
-  }
-};
-template <class T>
-struct PolicyKeep<T, false> {
-  uint4 u[POL_KEEP];
-  __device__ __forceinline__ PolicyKeep(uint8_t*) {}
-  __device__ __forceinline__ void fill(int j, const PolicyRowView<T, false>& row, int c) { u[j] = row.load(c); }
-  __device__ __forceinline__ void wait() {}
-  __device__ __forceinline__ const uint4& get(int j) const { return u[j]; }
+// exp(z - m) as exp2(z L - M), one fused operation and the exponential: M is
+// m L rounded to fp32, and the sum of such exponentials times correction() is
+// the sum of exp(z - m).  The product is exact inside the fused operation and
+// the difference is small where it counts, so large logits lose no digits.
+// Past 1e38 (rows whose logits are all the type's lowest) L is small enough for
+// M to be finite; there two different logits differ by 2^100 and more.
+struct PolicyExp {
+  float l, ml, m;
+  __device__ __forceinline__ explicit PolicyExp(float m_) : l(fabsf(m_) > 1e38f ? 0x1p-20f : LOG2E), ml(m_ * l), m(m_) {}
+  __device__ __forceinline__ float operator()(float z) const { return fast_exp2(fmaf(z, l, -ml)); }
+  __device__ __forceinline__ float correction() const { return fast_exp2(-fmaf(m, l, -ml)); }
 };
 
 // what one warp works out for a row from its maximum m, sum s = sum exp(z - m)
@@ -223,11 +206,11 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, const Polic
   return r;
 }
 
-// Rows first .. end-1 of a CTA: contiguous shares of equal cost, a row that is
+// Rows first .. end-1 of cluster `at` of n: contiguous shares of equal cost, a row that is
 // read and written counting 2, one that is only zeroed 1.  (With the same
-// number of rows for each CTA, 28 on average of which a third do not count,
-// the slowest CTA had a quarter more to do than the mean.)
-__device__ __forceinline__ int2 policy_share(const PolicyArgs& a, int* s_scan, int* s_range) {
+// number of rows for each, 28 on average of which a third do not count, the
+// slowest has a quarter more to do than the mean.)
+__device__ __forceinline__ int2 policy_share(const PolicyArgs& a, int at, int n, int* s_scan, int* s_range) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.rows + POL_THREADS - 1) / POL_THREADS;
   const int lo = min(a.rows, tid * per), hi = min(a.rows, lo + per);
@@ -248,13 +231,13 @@ __device__ __forceinline__ int2 policy_share(const PolicyArgs& a, int* s_scan, i
     total += s_scan[w];
   }
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {  // the row in which the cost reaches the CTA's bound
-    const int want = (int)((long long)(blockIdx.x + q) * total / gridDim.x);
+  for (int q = 0; q < 2; ++q) {  // the row in which the cost reaches the share's bound
+    const int want = (int)((long long)(at + q) * total / n);
     if (before <= want && want < before + mine) {
-      int at = before;
+      int sum = before;
       for (int i = lo; i < hi; ++i) {
-        at += a.weights[i] != 0.f ? 2 : 1;
-        if (want < at) {
+        sum += a.weights[i] != 0.f ? 2 : 1;
+        if (want < sum) {
           s_range[q] = i;
           break;
         }
@@ -266,41 +249,43 @@ __device__ __forceinline__ int2 policy_share(const PolicyArgs& a, int* s_scan, i
 }
 
 template <class T, bool ALIGNED>
-__global__ void __launch_bounds__(POL_THREADS, ALIGNED ? 3 : 2)
-    policy_rows_kernel(const T* logits, T* dlogits, PolicyArgs a) {
+__global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
+    policy_rows_kernel(const T* logits, T* dlogits, const PolicyArgs a) {
   constexpr int N = PolVec<T>::N;
+  using Row = PolicyRowView<T, ALIGNED>;
+  extern __shared__ __align__(16) uint4 pol_slots[];  // [POL_KEEP][POL_THREADS]
   __shared__ float sm[POL_WARPS], ss[POL_WARPS];
+  __shared__ float2 s_part[2];  // this CTA's maximum and sum of the row, by parity of the row
   __shared__ float s_g, s_inv;
   __shared__ int s_scan[POL_WARPS], s_range[2];
   __shared__ PolicyIn s_in[2];  // of rows i and i + 1, by parity
   __shared__ double s_sum[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % a.cs, at = blockIdx.x / a.cs, n = gridDim.x / a.cs;
+  uint4* slot = pol_slots + tid;  // slot j of this thread: slot[j * POL_THREADS]
   int first, end;
   if (a.weights) {
-    const int2 r = policy_share(a, s_scan, s_range);
+    const int2 r = policy_share(a, at, n, s_scan, s_range);
     first = r.x;
     end = r.y;
   } else {
-    first = (int)((long long)blockIdx.x * a.rows / gridDim.x);
-    end = (int)((long long)(blockIdx.x + 1) * a.rows / gridDim.x);
+    first = (int)((long long)at * a.rows / n);
+    end = (int)((long long)(at + 1) * a.rows / n);
   }
-  // f(j, c) for each kept vector: slot j of this thread, vector c of a row of `count`
-  const auto each = [&](int count, auto&& f) {
-    if constexpr (ALIGNED) {
-      const int n = min(POL_KEEP, (count - tid + POL_THREADS - 1) / POL_THREADS);  // (the same for every row)
-#pragma unroll 2
-      for (int j = 0; j < n; ++j) f(j, tid + j * POL_THREADS);
-    } else {
-#pragma unroll
-      for (int j = 0; j < POL_KEEP; ++j)  // (registers have to be named)
-        if (tid + j * POL_THREADS < count) f(j, tid + j * POL_THREADS);
-    }
-  };
   const auto view = [&](int i) {
-    return PolicyRowView<T, ALIGNED>(logits + (long long)i * a.ld, dlogits ? dlogits + (long long)i * a.ldd : nullptr, a.V);
+    return Row(logits + (long long)i * a.ld, dlogits ? dlogits + (long long)i * a.ldd : nullptr, a.V);
   };
-  extern __shared__ __align__(16) uint8_t pol_smem[];  // (ALIGNED)
-  PolicyKeep<T, ALIGNED> keep(pol_smem);
+  // this CTA's vectors of a row are lo(row) .. hi(row) - 1; thread t has lo + t, lo + t + POL_THREADS, ...
+  const auto lo = [&](const Row& r) { return (int)((long long)r.count * rank / a.cs); };
+  const auto hi = [&](const Row& r) { return (int)((long long)r.count * (rank + 1) / a.cs); };
+  // one asynchronous copy (ALIGNED)
+  const auto copy = [&](int j, const Row& r, int c) {
+    if (r.whole(c))
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot + j * POL_THREADS)),
+                   "l"(r.z + (long long)c * N) : "memory");
+    else
+      slot[j * POL_THREADS] = r.load(c);
+  };
   if (tid == 0) {
     s_sum[0] = s_sum[1] = s_sum[2] = 0.0;
     if (first < end) policy_in(a, first, &s_in[first & 1]);
@@ -309,67 +294,70 @@ __global__ void __launch_bounds__(POL_THREADS, ALIGNED ? 3 : 2)
   __syncthreads();
   bool have = false;  // the row is being loaded already
   for (int i = first; i < end; ++i) {
-    const PolicyRowView<T, ALIGNED> row = view(i);
+    const Row row = view(i);
+    const int c_lo = lo(row) + tid, c_hi = hi(row);
     const int y = s_in[i & 1].y;
     const float w = s_in[i & 1].w;
     if (tid == 0 && i + 1 < end) policy_in(a, i + 1, &s_in[(i + 1) & 1]);
     // (an action outside the vocabulary is reported, never read)
     if (w == 0.f || y < 0 || y >= a.V) {
       if (dlogits)
-        for (int c = tid; c < row.count; c += POL_THREADS) row.store(c, make_uint4(0, 0, 0, 0));
+        for (int c = c_lo; c < c_hi; c += POL_THREADS) row.store(c, make_uint4(0, 0, 0, 0));
       if (tid == 0) {
-        if (w != 0.f) record_error(ERRW_BAD_TARGET);
-        a.logp[i] = 0.f;
+        if (rank == 0) {
+          if (w != 0.f) record_error(ERRW_BAD_TARGET);
+          a.logp[i] = 0.f;
+        }
         policy_wait();
       }
       __syncthreads();
       continue;
     }
-    if (!have) each(row.count, [&](int j, int c) { keep.fill(j, row, c); });
-    have = false;
-    const float za = to_f(row.z[y]);
-    // this thread's maximum and sum of exponentials, then the row's
-    float m = -FLT_MAX;  // (so that a strip of -inf adds 0)
-    keep.wait();
-    each(row.count, [&](int j, int) { m = fmaxf(m, PolVec<T>::max(keep.get(j))); });
-    // exp2((z - m) log2 e) of elements k, k + 1 (z - m first: z log2 e alone
-    // would lose the digits of large logits, and overflow at the type's lowest)
-    unsigned long long m2 = f2_pack(-m, -m);
-    const unsigned long long l2 = f2_pack(LOG2E, LOG2E);
-    const auto exp_pair = [&](const uint4& w, int k) {
-      float lo, hi;
-      f2_unpack(f2_mul(f2_add(f2_pack(PolVec<T>::get(w, k), PolVec<T>::get(w, k + 1)), m2), l2), lo, hi);
-      return f2_pack(fast_exp2(lo), fast_exp2(hi));
-    };
-    unsigned long long s2 = 0;  // (0, 0)
-    const auto add = [&](const uint4& w) {
+    const int kept = max(0, min(POL_KEEP, (c_hi - c_lo + POL_THREADS - 1) / POL_THREADS));
+    const int c_rest = c_lo + POL_KEEP * POL_THREADS;  // the first vector that is not kept
+    if (!have) {
+      if constexpr (ALIGNED) {
+        for (int j = 0; j < kept; ++j) copy(j, row, c_lo + j * POL_THREADS);
+      } else {
+        for (int j0 = 0; j0 < kept; j0 += POL_BATCH) {
+          uint4 u[POL_BATCH];
 #pragma unroll
-      for (int k = 0; k < N; k += 2) s2 = f2_add(s2, exp_pair(w, k));
-    };
-    each(row.count, [&](int j, int) { add(keep.get(j)); });
-    // the rest of a long row in one pass, the sum rescaled when the maximum grows
-    for (int c0 = tid + POL_KEEP * POL_THREADS; c0 < row.count; c0 += POL_AHEAD * POL_THREADS) {
-      uint4 w[POL_AHEAD];
+          for (int q = 0; q < POL_BATCH; ++q)
+            if (j0 + q < kept) u[q] = row.load(c_lo + (j0 + q) * POL_THREADS);
 #pragma unroll
-      for (int q = 0; q < POL_AHEAD; ++q)
-        if (c0 + q * POL_THREADS < row.count) w[q] = row.load(c0 + q * POL_THREADS);
-#pragma unroll
-      for (int q = 0; q < POL_AHEAD; ++q) {
-        if (c0 + q * POL_THREADS < row.count) {
-          const float mx = PolVec<T>::max(w[q]);
-          if (mx > m) {
-            const float r = fast_exp2((m - mx) * LOG2E);
-            s2 = f2_mul(s2, f2_pack(r, r));
-            m = mx;
-            m2 = f2_pack(-m, -m);
-          }
-          add(w[q]);
+          for (int q = 0; q < POL_BATCH; ++q)
+            if (j0 + q < kept) slot[(j0 + q) * POL_THREADS] = u[q];
         }
       }
     }
-    float s, s_hi;
-    f2_unpack(s2, s, s_hi);
-    s += s_hi;
+    const float za = to_f(row.z[y]);
+    // this thread's maximum and sum of exponentials, then the row's
+    float m = -FLT_MAX;  // (so that a strip of -inf adds 0)
+    policy_wait();       // (this thread's copies)
+#pragma unroll 2
+    for (int j = 0; j < kept; ++j) m = fmaxf(m, PolVec<T>::max(slot[j * POL_THREADS]));
+    PolicyExp e(m);
+    float s4[4] = {0.f, 0.f, 0.f, 0.f};
+    const auto add = [&](const uint4& u) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) s4[k & 3] += e(PolVec<T>::get(u, k));
+    };
+#pragma unroll 2
+    for (int j = 0; j < kept; ++j) add(slot[j * POL_THREADS]);
+    // what is not kept, in one pass: the sums are rescaled when the maximum grows
+    for (int c = c_rest; c < c_hi; c += POL_THREADS) {
+      const uint4 u = row.load(c);
+      const float mx = PolVec<T>::max(u);
+      if (mx > m) {
+        const float r = fast_exp2((m - mx) * LOG2E) * e.correction();
+        m = mx;
+        e = PolicyExp(m);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s4[k] *= r / e.correction();
+      }
+      add(u);
+    }
+    float s = ((s4[0] + s4[1]) + (s4[2] + s4[3])) * e.correction();
     const float mw = warp_max(m);
     s = warp_sum(s * fast_exp2((m - mw) * LOG2E));
     if (lane == 0) {
@@ -377,17 +365,28 @@ __global__ void __launch_bounds__(POL_THREADS, ALIGNED ? 3 : 2)
       ss[warp] = s;
     }
     __syncthreads();
-    const float m_lane = sm[lane % POL_WARPS];
+    float m_lane = lane < POL_WARPS ? sm[lane] : -FLT_MAX;
     m = warp_max(m_lane);
-    m2 = f2_pack(-m, -m);
+    float S = 0.f;  // (warp 0)
+    if (warp == 0) S = warp_sum(lane < POL_WARPS ? ss[lane] * fast_exp2((m_lane - m) * LOG2E) : 0.f);
+    if (a.cs > 1) {  // the cluster's: each CTA reads the others' parts
+      if (tid == 0) s_part[i & 1] = make_float2(m, S);
+      cluster_sync_all();
+      float2 part = make_float2(-FLT_MAX, 0.f);
+      if (lane < a.cs)
+        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(part.x), "=f"(part.y)
+                     : "r"(map_shared_rank(&s_part[i & 1], lane)) : "memory");
+      m = warp_max(part.x);
+      S = warp_sum(part.y * fast_exp2((part.x - m) * LOG2E));
+    }
+    e = PolicyExp(m);
     if (warp == 0) {
-      const float S = warp_sum(lane < POL_WARPS ? ss[lane] * fast_exp2((m_lane - m) * LOG2E) : 0.f);
       const PolicyRow r = policy_row(a, s_in[i & 1], m, S, za);
       if (lane == 0) {
         s_sum[0] += r.loss;
         s_sum[1] += r.kl;
         s_sum[2] += r.clipped;
-        a.logp[i] = (float)r.lp;
+        if (rank == 0) a.logp[i] = (float)r.lp;
         s_g = (float)r.g;
         s_inv = (float)(-r.g / (double)S);
         policy_wait();  // the next row's scalars
@@ -395,49 +394,51 @@ __global__ void __launch_bounds__(POL_THREADS, ALIGNED ? 3 : 2)
     }
     __syncthreads();
     if (!dlogits) continue;
-    const float g = s_g, inv = s_inv;
-    const unsigned long long i2 = f2_pack(inv, inv);
-    const auto grad = [&](int c, const uint4& w) {
+    const float inv = s_inv * e.correction();
+    const auto grad = [&](int c, const uint4& u) {
       float v[N];
 #pragma unroll
-      for (int k = 0; k < N; k += 2) f2_unpack(f2_mul(exp_pair(w, k), i2), v[k], v[k + 1]);
+      for (int k = 0; k < N; ++k) v[k] = e(PolVec<T>::get(u, k)) * inv;
       row.store(c, PolVec<T>::pack(v));
     };
-    // the rest of a long row first, while its logits are still in L2; then what
-    // was kept, each slot refilled from the next row as its gradient leaves
-    for (int c0 = tid + POL_KEEP * POL_THREADS; c0 < row.count; c0 += POL_AHEAD * POL_THREADS) {
-      uint4 w[POL_AHEAD];
-#pragma unroll
-      for (int q = 0; q < POL_AHEAD; ++q)
-        if (c0 + q * POL_THREADS < row.count) w[q] = row.load(c0 + q * POL_THREADS);
-#pragma unroll
-      for (int q = 0; q < POL_AHEAD; ++q)
-        if (c0 + q * POL_THREADS < row.count) grad(c0 + q * POL_THREADS, w[q]);
-    }
+    // what was not kept first, while it is still in L2; then the slots, each
+    // refilled from the next row as its gradient leaves
+    for (int c = c_rest; c < c_hi; c += POL_THREADS) grad(c, row.load(c));
     const PolicyIn& in = s_in[(i + 1) & 1];
     have = i + 1 < end && in.w != 0.f && in.y >= 0 && in.y < a.V;
-    const PolicyRowView<T, ALIGNED> next = view(have ? i + 1 : i);
     if constexpr (ALIGNED) {
-      each(row.count, [&](int j, int c) {
-        grad(c, keep.get(j));
-        if (have) keep.fill(j, next, c);
-      });
+      const T* shift = logits + (long long)(i + 1) * a.ld;
+      const Row next(shift, dlogits, a.V);  // (the vectors lie alike in every row)
+#pragma unroll 2
+      for (int j = 0; j < kept; ++j) {
+        grad(c_lo + j * POL_THREADS, slot[j * POL_THREADS]);
+        if (have) copy(j, next, c_lo + j * POL_THREADS);
+      }
     } else {
+      const Row next = view(have ? i + 1 : i);
+      const int n_lo = lo(next) + tid, n_hi = have ? hi(next) : n_lo;
+      for (int j0 = 0; j0 < POL_KEEP; j0 += POL_BATCH) {
+        uint4 u[POL_BATCH];
 #pragma unroll
-      for (int j = 0; j < POL_KEEP; ++j) {
-        const int c = tid + j * POL_THREADS;
-        if (c < row.count) grad(c, keep.get(j));
-        if (have && c < next.count) keep.fill(j, next, c);
+        for (int q = 0; q < POL_BATCH; ++q)
+          if (j0 + q < POL_KEEP && n_lo + (j0 + q) * POL_THREADS < n_hi) u[q] = next.load(n_lo + (j0 + q) * POL_THREADS);
+#pragma unroll
+        for (int q = 0; q < POL_BATCH; ++q) {
+          if (j0 + q < kept) grad(c_lo + (j0 + q) * POL_THREADS, slot[(j0 + q) * POL_THREADS]);
+          if (j0 + q < POL_KEEP && n_lo + (j0 + q) * POL_THREADS < n_hi) slot[(j0 + q) * POL_THREADS] = u[q];
+        }
       }
     }
     // the action's own element, by the thread that wrote its vector
-    if (tid == (y + row.p) / N % POL_THREADS)
-      row.dz[y] = from_f<T>(fmaf(fast_exp2((za - m) * LOG2E), inv, g));
+    const int c_y = (y + row.p) / N;
+    if (c_y >= c_lo && c_y < c_hi && (c_y - c_lo) % POL_THREADS == 0)
+      row.dz[y] = from_f<T>(fmaf(e(za), inv, s_g));
   }
-  if (tid < 3 && a.part) a.part[blockIdx.x * 3 + tid] = s_sum[tid];
+  if (rank == 0 && tid < 3 && a.part) a.part[at * 3 + tid] = s_sum[tid];
+  if (a.cs > 1) cluster_sync_all();  // no CTA leaves while another may read its part
 }
 
-// the CTAs' sums, added in a fixed order: one warp per statistic
+// the clusters' sums, added in a fixed order: one warp per statistic
 __global__ void __launch_bounds__(96) policy_stats_kernel(const double* __restrict__ part, int n, float* __restrict__ stats) {
   const int q = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double v = 0.0;
