@@ -209,6 +209,21 @@ int allow_smem(K kernel, int bytes, SmemOnce& once) {
 }
 SmemOnce g_smem_packed_fwd, g_smem_packed_bwd, g_smem_prefix;
 
+// a kernel that begins with pdl_wait(), set up while the one before it in the stream ends
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // --------------------------------------------------------------- GEMM ----
 struct Op {
   const void* p;
@@ -1636,7 +1651,7 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
     return GPTB_ERR_INVALID_ARG;
   if (H / Hkv > 128) return GPTB_ERR_UNSUPPORTED;
   const long long tiles = (long long)B * Hkv * ((T_max + 127) / 128 + ((long long)total_prefix + 127) / 128);
-  if (tiles > (1ll << 30) || (long long)B * T_max > (1ll << 30) || (long long)B * H > (1ll << 30) ||
+  if (tiles > (1ll << 26) || (long long)B * T_max > (1ll << 30) || (long long)B * H > (1ll << 30) ||
       total_prefix > (1 << 30))
     return GPTB_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace)) return GPTB_ERR_INVALID_ARG;
@@ -1688,7 +1703,9 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
   TRY(allow_smem(prefix_split_kernel, PD_SMEM, g_smem_prefix));
   prefix_split_kernel<<<grid, PD_THREADS, PD_SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, a);
   CKL();
-  prefix_combine_kernel<<<(unsigned)(((long long)B * H + 3) / 4), 128, 0, st>>>(a, static_cast<bf16*>(o), lse, grid);
+  // set up while the split kernel ends
+  CK(launch_dependent(prefix_combine_kernel, (unsigned)(B * H), 128, st, a, static_cast<bf16*>(o),
+                      lse, grid));
   CKL();
   return GPTB_OK;
 }

@@ -17,13 +17,20 @@
 //
 // Work: a "segment" is one (query rows, kv head, prefix or own cache); its
 // keys are cut into 128-row tiles.  The tiles of all segments, laid end to end,
-// are dealt out evenly and contiguously over the CTAs (every CTA computes the
-// same prefix sum over the batch from lens and the offsets), so lengths that
-// differ by any factor load every SM alike.  A segment that spans several CTAs
-// leaves one partial softmax (max, sum, o) per CTA -- and per CTA two, as the
-// even and odd tiles go to two softmax groups with an accumulator each -- and
+// are dealt out contiguously over the CTAs by cost (every CTA computes the same
+// prefix sum over the batch from lens and the offsets), so lengths that differ
+// by any factor load every SM alike.  A segment that spans several CTAs leaves
+// one partial softmax (max, sum, o) per CTA -- and per CTA two, as the even and
+// odd tiles go to two softmax groups with an accumulator each -- and
 // prefix_combine_kernel joins them.  The dealing is fixed by the lengths, so
 // results do not vary from run to run.
+//
+// A tile's loads take 2.4 us to arrive with HBM busy, so K and V have a ring
+// each, and the producer issues whichever has a free stage (in turn, K waited
+// for the V stage before it: 2600 cycles per tile); and the query rows of
+// several segments lie in shared memory side by side: the matrix product reads
+// 128 rows from the first of them on, and what lies behind makes rows of S that
+// nobody reads.
 #pragma once
 #include "attention_tc.cuh"
 #include "common.cuh"
@@ -31,12 +38,20 @@
 
 namespace gptb {
 
-constexpr int PD_THREADS = 320;
+constexpr int PD_THREADS = 384;   // warps 0-7 softmax, 10 producer, 11 MMA issuer
+// (the producer polls: on the scheduler of the warps that hold TMEM lanes 0-31,
+// the only ones with rows in most segments, it would take their issue slots)
+constexpr int PD_PRODUCER = 10, PD_MMA = 11;
 constexpr int PD_MAX_CTAS = 160;
-constexpr int PD_TILE = FA_TILE;     // 128 rows x 128 columns, bf16: two 64-column swizzled halves
-constexpr int PD_BOX = 32;           // rows per TMA box (a short last tile loads only the boxes it needs)
-constexpr int PD_RING = 8;           // tile descriptors in flight (more than the K / V stages)
-constexpr int PD_SMEM = 1024 + 2 * PD_TILE /*Q*/ + 4 * PD_TILE /*K, V x2*/;
+constexpr int PD_TILE = FA_TILE;  // 128 rows x 128 columns, bf16: two 64-column swizzled halves
+constexpr int PD_BOX = 32;        // rows per TMA box (a short last tile loads only the boxes it needs)
+constexpr int PD_ST = 3;          // K / V stages
+constexpr int PD_RING = 8;        // tile descriptors in flight (more than the K / V stages)
+constexpr int PD_QS = 8;          // segments whose query rows can be in shared memory, in 16 units of 8 rows
+constexpr int PD_SMEM = 1024 + PD_TILE /*Q*/ + 2 * PD_ST * PD_TILE;
+// cost of a segment: its tiles, and PD_OPEN units more (query rows to load, an
+// accumulator to read out) that go with its first tile
+constexpr int PD_UNIT = 4, PD_OPEN = 2;
 constexpr int PD_REC = 132;          // floats of a partial result: o[128], max (base 2), sum, 2 unused
 
 enum : int {
@@ -53,15 +68,16 @@ struct PdTile {
   int pos;    // position of the first key
   int b0, nrows, kvh;
   int plen;   // prefix length of the group
-  int pad;
+  int q;      // first 8-row unit of the segment's query rows
+  int row;    // first row of the tile in the prefix or the cache
 };
 
 struct PrefixArgs {
   const int32_t *cu_prefix, *cu_group, *lens;
   int total_prefix, n_groups, B, H, Hkv, T_max, window;
   int spt;       // sequences per query tile of a prefix segment (128 / G)
-  int4* plan;    // [B + 1]: first tile of the sequence's segments, prefix tiles, own tiles (-1: bad length), first
-                 // sequence of its query tile; [B].x = all tiles
+  int4* plan;    // [B + 1]: first cost unit of the sequence's segments, prefix tiles, own tiles (-1: bad length),
+                 // first sequence of its query tile; [B].x = all units
   float* rec_a;  // [2 sources][B*H][2][PD_REC] the share of a segment that starts it
   float* rec_b;  // [CTAs][rows of a query tile][2][PD_REC] the share of the segment that a CTA goes on with
 };
@@ -108,9 +124,48 @@ __device__ __forceinline__ PdSeq pd_seq(const PrefixArgs& a, int b) {
   return s;
 }
 
-// tile range of CTA c of n: [pd_begin(c), pd_begin(c + 1)); pd_owner(f): the CTA that has tile f
-__device__ __forceinline__ int pd_begin(int c, int n, int W) { return (int)((long long)c * W / n); }
-__device__ __forceinline__ int pd_owner(int f, int n, int W) { return (int)((((long long)f + 1) * n - 1) / W); }
+// units of a segment of nt tiles; the first tile whose units begin at u (relative to the segment) or later
+__device__ __forceinline__ int pd_units(int nt) { return nt > 0 ? PD_UNIT * nt + PD_OPEN : 0; }
+__device__ __forceinline__ int pd_tile(int u) {
+  return u <= 0 ? 0 : u <= PD_OPEN + PD_UNIT ? 1 : (u - PD_OPEN + PD_UNIT - 1) / PD_UNIT;
+}
+// CTA c of n has the tiles that begin in the units [pd_begin(c), pd_begin(c + 1)) of U; pd_owner(u): the CTA of unit u
+// (n <= PD_MAX_CTAS; a 64-bit division costs ten times a 32-bit one)
+__device__ __forceinline__ int pd_begin(int c, int n, int U) {
+  return U < (1 << 24) ? (int)((uint32_t)c * (uint32_t)U / (uint32_t)n) : (int)((long long)c * U / n);
+}
+__device__ __forceinline__ int pd_owner(int u, int n, int U) {
+  return U < (1 << 24) ? (int)((((uint32_t)u + 1u) * (uint32_t)n - 1u) / (uint32_t)U)
+                       : (int)((((long long)u + 1) * n - 1) / U);
+}
+
+// f(seq, b, own, kvh, j0, j1) for every segment with tiles in the units [u0,
+// u1): its tiles j0 .. j1-1.  The walk starts at sequence b, whose segments
+// start at unit `base`, and ends early when f returns false.  By a whole warp,
+// whose lanes look up 32 sequences at once.
+template <class F>
+__device__ __forceinline__ bool pd_walk(const PrefixArgs& a, int b, int base, int u0, int u1, F&& f) {
+  const int lane = threadIdx.x & 31;
+  PdSeq block;
+  for (int at_lane = 0; b < a.B && base < u1; ++b, ++at_lane) {
+    if ((at_lane & 31) == 0) block = pd_seq(a, min(b + lane, a.B - 1));
+    const auto get = [&](int v) { return __shfl_sync(0xffffffffu, v, at_lane & 31); };
+    const PdSeq s{get(block.p0), get(block.plen), get(block.b0), get(block.nseq), get(block.plo),
+                  get(block.ntp), get(block.len), get(block.olo), get(block.nto)};
+    for (int own = 0; own < 2; ++own) {
+      const int nt = own ? s.nto : s.ntp, len = pd_units(nt);
+      if (nt == 0) continue;
+      for (int kvh = u0 > base ? (u0 - base) / len : 0; kvh < a.Hkv; ++kvh) {
+        const int at = base + kvh * len;
+        if (at >= u1) break;
+        const int j0 = pd_tile(u0 - at), j1 = min(nt, pd_tile(u1 - at));
+        if (j0 < j1 && !f(s, b, own != 0, kvh, j0, j1)) return false;
+      }
+      base += a.Hkv * len;
+    }
+  }
+  return true;
+}
 
 __global__ void __launch_bounds__(PD_THREADS, 1)
     prefix_split_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_qo,
@@ -119,24 +174,24 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
                         const PrefixArgs a) {
   extern __shared__ uint8_t pd_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pd_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;              // 2 segments' query tiles
-  uint8_t* sK = sQ + 2 * PD_TILE;  // 2 stages
-  uint8_t* sV = sK + 2 * PD_TILE;  // 2 stages
-  __shared__ __align__(8) uint64_t bars[24];
-  uint64_t* q_full = bars + 0;    // [2]
-  uint64_t* q_empty = bars + 2;   // [2]
-  uint64_t* k_full = bars + 4;    // [2]
-  uint64_t* k_empty = bars + 6;   // [2]
-  uint64_t* v_full = bars + 8;    // [2]
-  uint64_t* v_empty = bars + 10;  // [2]
-  uint64_t* s_full = bars + 12;   // [2 groups]
-  uint64_t* p_full = bars + 14;   // [2 groups]
-  uint64_t* o_done = bars + 16;   // [2 groups]
-  uint64_t* o_free = bars + 18;   // [2 groups] the accumulator has been read out
-  uint64_t* drain = bars + 20;
+  uint8_t* sQ = smem;                  // one or two segments' query rows
+  uint8_t* sK = sQ + PD_TILE;          // PD_ST stages
+  uint8_t* sV = sK + PD_ST * PD_TILE;  // PD_ST stages
+  __shared__ __align__(8) uint64_t bars[9 + 4 * PD_ST + 2 * PD_QS];
+  uint64_t* s_full = bars + 0;             // [2 groups]
+  uint64_t* p_full = bars + 2;             // [2 groups]
+  uint64_t* o_done = bars + 4;             // [2 groups]
+  uint64_t* o_free = bars + 6;             // [2 groups] the accumulator has been read out
+  uint64_t* drain = bars + 8;
+  uint64_t* k_full = bars + 9;             // [PD_ST]
+  uint64_t* k_empty = k_full + PD_ST;      // [PD_ST]
+  uint64_t* v_full = k_full + 2 * PD_ST;   // [PD_ST]
+  uint64_t* v_empty = k_full + 3 * PD_ST;  // [PD_ST]
+  uint64_t* q_full = k_full + 4 * PD_ST;   // [PD_QS]
+  uint64_t* q_empty = q_full + PD_QS;      // [PD_QS]
   __shared__ PdTile ring[PD_RING];
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_abort, s_sum[PD_THREADS / 32], s_b, s_off;
+  __shared__ int s_abort, s_sum[PD_THREADS / 32], s_b, s_base;
   volatile int* abort_flag = &s_abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -145,21 +200,25 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 1);
-      mbar_init(&q_empty[i], 1);
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
       mbar_init(&o_done[i], 1);
       mbar_init(&o_free[i], 4);
     }
+    for (int i = 0; i < PD_ST; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+    }
+    for (int i = 0; i < PD_QS; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+    }
     mbar_init(drain, 1);
     s_abort = 0;
-    s_b = 0;
-    s_off = 0;
+    s_b = a.B;
+    s_base = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tm_qp);
     tma_prefetch_desc(&tm_qo);
@@ -168,15 +227,15 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     tma_prefetch_desc(&tm_ko);
     tma_prefetch_desc(&tm_vo);
   }
-  if (warp == 1) tmem_alloc(&tmem_slot, 512);
+  if (warp == PD_MMA) tmem_alloc(&tmem_slot, 512);
 
-  // the batch's tiles, summed up: thread i has the sequences i*per .. of the batch
+  // the batch's cost, summed up: thread i has the sequences i*per .. of the batch
   const int per = (a.B + PD_THREADS - 1) / PD_THREADS;
   const int b_lo = min(a.B, (int)threadIdx.x * per), b_hi = min(a.B, b_lo + per);
   int mine = 0;
   for (int b = b_lo; b < b_hi; ++b) {
     const PdSeq s = pd_seq(a, b);
-    mine += a.Hkv * (s.ntp + s.nto);
+    mine += a.Hkv * (pd_units(s.ntp) + pd_units(s.nto));
   }
   int inc = mine;  // inclusive sum over the warp's lanes
 #pragma unroll
@@ -189,27 +248,28 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  int before = inc - mine, W = 0;
+  int before = inc - mine, U = 0;
   for (int w = 0; w < PD_THREADS / 32; ++w) {
     if (w < warp) before += s_sum[w];
-    W += s_sum[w];
+    U += s_sum[w];
   }
-  const int f0 = pd_begin(cta, nctas, W), f1 = pd_begin(cta + 1, nctas, W);
-  if (cta == 0 || (before <= f0 && f0 < before + mine)) {
-    int f = before;
+  const int u0 = pd_begin(cta, nctas, U), u1 = pd_begin(cta + 1, nctas, U);
+  if (cta == 0 || (before <= u0 && u0 < before + mine)) {
+    int u = before;
     for (int b = b_lo; b < b_hi; ++b) {
       const PdSeq s = pd_seq(a, b);
-      const int n = a.Hkv * (s.ntp + s.nto);
-      if (f <= f0 && f0 < f + n) {  // this CTA's first tile
+      const int n = a.Hkv * (pd_units(s.ntp) + pd_units(s.nto));
+      if (u <= u0 && u0 < u + n) {  // this CTA's first unit
         s_b = b;
-        s_off = f0 - f;
+        s_base = u;
       }
-      if (cta == 0) a.plan[b] = make_int4(f, s.ntp, s.len < 0 ? -1 : s.nto, s.b0);
-      f += n;
+      if (cta == 0) a.plan[b] = make_int4(u, s.ntp, s.len < 0 ? -1 : s.nto, s.b0);
+      u += n;
     }
   }
+  pdl_launch();  // (prefix_combine_kernel's CTAs take the place of those that end, and wait for the rest)
   if (cta == 0) {
-    if (threadIdx.x == 0) a.plan[a.B] = make_int4(W, 0, 0, 0);
+    if (threadIdx.x == 0) a.plan[a.B] = make_int4(U, 0, 0, 0);
     if (a.n_groups > 0) {
       packed_check(a.cu_prefix, a.n_groups, a.total_prefix);
       packed_check(a.cu_group, a.n_groups, a.B);
@@ -217,123 +277,160 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   }
   __syncthreads();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int left = f1 - f0, b = s_b, off = s_off, n = 0, seg = 0;
-      bool ok = true;
-      PdSeq s;
-      if (left > 0) s = pd_seq(a, b);
-      while (ok && left > 0) {
-        const int np = a.Hkv * s.ntp;
-        const bool own = off >= np;
-        const int nt = own ? s.nto : s.ntp;
-        const int at = own ? off - np : off;
-        if (nt == 0 || at >= a.Hkv * nt) {  // the next sequence
-          if (++b >= a.B) break;
-          off = 0;
-          s = pd_seq(a, b);
-          continue;
+  if (warp == PD_PRODUCER) {
+    // -------------------------------------------- producer (the whole warp)
+    {
+      int n = 0, nv = 0, seg = 0;    // K tiles, V tiles and segments so far
+      int q_at = 0, q_used = 0;      // next free unit of sQ; units in use
+      int q_old = 0;                 // the oldest segment in sQ
+      unsigned long long q_len = 0;  // units (8 bits) of the segments q_old, q_old + 1, ... in sQ, and skipped before them
+      // one tile's rows (those boxes that hold keys) into a stage, a box by each lane
+      const auto load = [&](const PdTile& d, uint8_t* to, uint64_t* bar, const CUtensorMap* map) {
+        const int boxes = (d.nk + PD_BOX - 1) / PD_BOX;
+        if (lane == 0) mbar_arrive_expect_tx(bar, boxes * 2 * PD_BOX * 128);
+        __syncwarp();
+        const int x = lane >> 1, half = lane & 1;
+        if (x < boxes)
+          tma_load_2d(to + half * 16384 + x * PD_BOX * 128, map, bar, d.kvh * 128 + half * 64, d.row + x * PD_BOX);
+      };
+      const auto ready = [&](uint64_t* bar, uint32_t parity) {  // (the same answer in all lanes)
+        return __all_sync(0xffffffffu, mbar_test_wait(bar, parity)) != 0;
+      };
+      // the V tiles whose stages are free, up to the last K tile
+      const auto pump = [&]() {
+        while (nv < n && ready(&v_empty[nv % PD_ST], ((nv / PD_ST) & 1) ^ 1u)) {
+          const PdTile d = ring[nv % PD_RING];
+          load(d, sV + nv % PD_ST * PD_TILE, &v_full[nv % PD_ST], d.flags & PD_OWN ? &tm_vo : &tm_vp);
+          ++nv;
         }
-        const int kvh = at / nt, t0 = at - kvh * nt;
-        const int cnt = min(nt - t0, left);
-        // the segment's query rows
-        const int qs = seg & 1;
-        ok = mbar_wait(&q_empty[qs], ((seg >> 1) & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_PRODUCER);
-        if (!ok) break;
-        uint8_t* q = sQ + qs * PD_TILE;
+      };
+      // bounded as mbar_wait, issuing V tiles meanwhile; bar NULL: until all V tiles are issued
+      const auto wait = [&](uint64_t* bar, uint32_t parity) {
+        unsigned long long t0 = 0;
+        for (uint32_t i = 0;; ++i) {
+          if (bar ? ready(bar, parity) : nv == n) return true;
+          pump();
+          if ((i & 255u) == 255u) {
+            const unsigned long long now = __shfl_sync(0xffffffffu, globaltimer_ns(), 0);
+            if (t0 == 0) t0 = now;
+            const bool late = now - t0 > g_wait_limit_ns;
+            if (late && lane == 0) {
+              record_error(ERRW_TIMEOUT_PRODUCER);
+              *abort_flag = 1;
+            }
+            __syncwarp();
+            if (__any_sync(0xffffffffu, late || *abort_flag)) return false;
+          }
+        }
+      };
+      const auto segment = [&](const PdSeq& s, int b, bool own, int kvh, int j0, int j1) {
+        // room for its query rows, in one piece; the oldest leave first
+        const int nseq = own ? 1 : a.spt, need = (nseq * G + 7) / 8;
+        bool wrap;
+        int skip;
+        while (true) {
+          if (q_used == 0) q_at = 0;
+          wrap = q_at + need > 16;
+          skip = wrap ? 16 - q_at : 0;
+          if (q_used + skip + need <= 16 && seg - q_old < PD_QS) break;
+          if (!wait(&q_empty[q_old % PD_QS], (q_old / PD_QS) & 1)) return false;
+          q_used -= (int)(q_len & 255);
+          q_len >>= 8;
+          ++q_old;
+        }
+        const int at = wrap ? 0 : q_at;
+        q_len |= (unsigned long long)(skip + need) << (8 * (seg - q_old));
+        q_used += skip + need;
+        q_at = at + need;
+        uint64_t* qf = &q_full[seg % PD_QS];
         const CUtensorMap* mq = own ? &tm_qo : &tm_qp;
-        mbar_arrive_expect_tx(&q_full[qs], 2 * 128 * G * (own ? 1 : a.spt));
-        tma_load_3d(q, mq, &q_full[qs], 0, kvh * G, b);
-        tma_load_3d(q + 16384, mq, &q_full[qs], 64, kvh * G, b);
-        const CUtensorMap *mk = own ? &tm_ko : &tm_kp, *mv = own ? &tm_vo : &tm_vp;
-        const int first = own ? s.olo : s.plo, rows = own ? s.len : s.plen;
-        const int base = own ? b * a.T_max : s.p0;
-        for (int j = 0; j < cnt; ++j, ++n) {
-          const int st = n & 1;
-          const uint32_t par = ((n >> 1) & 1) ^ 1u;
-          const int r0 = first + (t0 + j) * FA_BN;
-          PdTile d;
-          d.nk = min(FA_BN, rows - r0);
-          d.flags = (j == 0 ? PD_FIRST_SEG : 0) | (j == cnt - 1 ? PD_LAST_SEG : 0) | (j < 2 ? PD_FIRST_ACC : 0) |
-                    (j >= cnt - 2 ? PD_LAST_ACC : 0) | (t0 > 0 ? PD_CONT : 0) | (own ? PD_OWN : 0) |
-                    (j & 1 ? PD_ODD : 0);
-          d.pos = own ? s.plen + r0 : r0;
-          d.b0 = b;
-          d.nrows = own ? G : s.nseq * G;
-          d.kvh = kvh;
-          d.plen = s.plen;
-          const int boxes = (d.nk + PD_BOX - 1) / PD_BOX;
-          ok = mbar_wait(&k_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER);
-          if (!ok) break;
-          // (the ring's entry was last read by the softmax of tile n - PD_RING,
-          // before the PV product whose end freed the V stage of tile n - 1)
-          ring[n % PD_RING] = d;
-          mbar_arrive_expect_tx(&k_full[st], boxes * 2 * PD_BOX * 128);
-          uint8_t* k = sK + st * PD_TILE;
-          for (int x = 0; x < boxes; ++x) {
-            tma_load_2d(k + x * PD_BOX * 128, mk, &k_full[st], kvh * 128, base + r0 + x * PD_BOX);
-            tma_load_2d(k + 16384 + x * PD_BOX * 128, mk, &k_full[st], kvh * 128 + 64, base + r0 + x * PD_BOX);
-          }
-          ok = mbar_wait(&v_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER);
-          if (!ok) break;
-          mbar_arrive_expect_tx(&v_full[st], boxes * 2 * PD_BOX * 128);
-          uint8_t* v = sV + st * PD_TILE;
-          for (int x = 0; x < boxes; ++x) {
-            tma_load_2d(v + x * PD_BOX * 128, mv, &v_full[st], kvh * 128, base + r0 + x * PD_BOX);
-            tma_load_2d(v + 16384 + x * PD_BOX * 128, mv, &v_full[st], kvh * 128 + 64, base + r0 + x * PD_BOX);
-          }
-        }
-        off += cnt;
-        left -= cnt;
+        if (lane == 0) mbar_arrive_expect_tx(qf, 2 * 128 * G * nseq);
+        __syncwarp();
+        if (lane < 2) tma_load_3d(sQ + lane * 16384 + at * 1024, mq, qf, lane * 64, kvh * G, b);
         ++seg;
-      }
-      // the end of the stream, for both softmax groups
-      if (ok && mbar_wait(&k_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_PRODUCER)) {
-        ring[n % PD_RING].flags = PD_END;
-        ring[(n + 1) % PD_RING].flags = PD_END;
-        mbar_arrive(&k_full[n & 1]);
+        PdTile d;
+        d.b0 = b;
+        d.nrows = own ? G : s.nseq * G;
+        d.kvh = kvh;
+        d.plen = s.plen;
+        d.q = at;
+        const int first = own ? s.olo : s.plo, rows = own ? s.len : s.plen, base = own ? b * a.T_max : s.p0;
+        for (int j = j0; j < j1; ++j) {
+          const int r0 = first + j * FA_BN;
+          d.nk = min(FA_BN, rows - r0);
+          d.flags = (j == j0 ? PD_FIRST_SEG : 0) | (j == j1 - 1 ? PD_LAST_SEG : 0) | (j < j0 + 2 ? PD_FIRST_ACC : 0) |
+                    (j >= j1 - 2 ? PD_LAST_ACC : 0) | (j0 > 0 ? PD_CONT : 0) | (own ? PD_OWN : 0) |
+                    ((j - j0) & 1 ? PD_ODD : 0);
+          d.pos = own ? s.plen + r0 : r0;
+          d.row = base + r0;
+          if (!wait(&k_empty[n % PD_ST], ((n / PD_ST) & 1) ^ 1u)) return false;
+          // The ring's entry was last read by the softmax of tile n - PD_RING:
+          // this stage was freed by S of tile n - PD_ST, issued after the PV
+          // product of tile n - PD_ST - 2, and so after that tile's softmax
+          // and the issue of its V.
+          if (lane == 0) ring[n % PD_RING] = d;
+          __syncwarp();
+          load(d, sK + n % PD_ST * PD_TILE, &k_full[n % PD_ST], own ? &tm_ko : &tm_kp);
+          ++n;
+          pump();
+        }
+        return true;
+      };
+      // then the end of the stream, for both softmax groups
+      if (pd_walk(a, s_b, s_base, u0, u1, segment) && wait(nullptr, 0) &&
+          wait(&k_empty[n % PD_ST], ((n / PD_ST) & 1) ^ 1u)) {
+        if (lane == 0) {
+          ring[n % PD_RING].flags = PD_END;
+          ring[(n + 1) % PD_RING].flags = PD_END;
+          mbar_arrive(&k_full[n % PD_ST]);
+        }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == PD_MMA) {
     // ---------------------------------------------------------- MMA issuer
-    // S_t = Q K^T of tile n (t = n % 2) is issued one tile ahead of O_t += P_t V
+    // S_t = Q K^T of tile n (t = n % 2) is issued one tile ahead of O_t += P_t V.
+    // A short tile takes the keys it has, in steps of 16.
     if (lane == 0) {
-      constexpr uint32_t IDESC_S = make_idesc(128, 128, false, false, false);
+      constexpr uint32_t IDESC_S = make_idesc(128, 0, false, false, false);  // + N
       constexpr uint32_t IDESC_O = make_idesc(128, 128, false, true, false);
       int seg = -1, used[2] = {0, 0};
       bool ok = true, end = false;
+      int steps = 0, q_unit = 0;  // 16-key steps of the tile whose S was issued last; its segment's query rows
       auto issue_s = [&](int n) -> int {
-        const int t = n & 1;
-        ok = mbar_wait(&k_full[t], (n >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA);
+        const int t = n & 1, st = n % PD_ST;
+        ok = mbar_wait(&k_full[st], (n / PD_ST) & 1, abort_flag, ERRW_TIMEOUT_MMA);
         if (!ok) return 0;
-        const int fl = *reinterpret_cast<volatile int*>(&ring[n % PD_RING].flags);
+        const volatile PdTile& d = ring[n % PD_RING];
+        const int fl = d.flags;
         if (fl & PD_END) {
           end = true;
           return fl;
         }
         if (fl & PD_FIRST_SEG) {
           ++seg;
-          ok = mbar_wait(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA);
+          q_unit = d.q;
+          ok = mbar_wait(&q_full[seg % PD_QS], (seg / PD_QS) & 1, abort_flag, ERRW_TIMEOUT_MMA);
           if (!ok) return 0;
         }
+        steps = (d.nk + 15) >> 4;
         tc_fence_after();
-        const uint32_t aQ = smem_u32(sQ + (seg & 1) * PD_TILE), aK = smem_u32(sK + t * PD_TILE);
+        const uint32_t aQ = smem_u32(sQ + q_unit * 1024), aK = smem_u32(sK + st * PD_TILE);
+        const uint32_t idesc = IDESC_S | (uint32_t)(2 * steps) << 17;  // N = 16 steps
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_bf16_ss(tmem + t * 128, fa_desc_k(aQ, k), fa_desc_k(aK, k), IDESC_S, k > 0 ? 1u : 0u);
+          mma_bf16_ss(tmem + t * 128, fa_desc_k(aQ, k), fa_desc_k(aK, k), idesc, k > 0 ? 1u : 0u);
         mma_commit(&s_full[t]);
-        mma_commit(&k_empty[t]);
-        if (fl & PD_LAST_SEG) mma_commit(&q_empty[seg & 1]);
+        mma_commit(&k_empty[st]);
+        if (fl & PD_LAST_SEG) mma_commit(&q_empty[seg % PD_QS]);
         return fl;
       };
       int fl = issue_s(0);
       for (int n = 0; ok && !end; ++n) {
-        const int t = n & 1;
-        const int fl_n = fl;
+        const int t = n & 1, st = n % PD_ST;
+        const int fl_n = fl, steps_n = steps;
         fl = issue_s(n + 1);
         if (!ok) break;
-        if (!mbar_wait(&v_full[t], (n >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA) ||
+        if (!mbar_wait(&v_full[st], (n / PD_ST) & 1, abort_flag, ERRW_TIMEOUT_MMA) ||
             !mbar_wait(&p_full[t], (n >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA) ||
             ((fl_n & PD_FIRST_ACC) &&
              !mbar_wait(&o_free[t], (used[t]++ & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_MMA))) {
@@ -341,12 +438,11 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t aV = smem_u32(sV + t * PD_TILE);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
+        const uint32_t aV = smem_u32(sV + st * PD_TILE);
+        for (int k = 0; k < steps_n; ++k)
           mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, fa_desc_mn(aV, k), IDESC_O,
                       (k > 0 || !(fl_n & PD_FIRST_ACC)) ? 1u : 0u);
-        mma_commit(&v_empty[t]);
+        mma_commit(&v_empty[st]);
         mma_commit(&o_done[t]);
       }
       if (ok) {  // both groups have taken their last tile: they read the end mark
@@ -360,9 +456,9 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           if (globaltimer_ns() - t0 > 100000000ull) { record_error(ERRW_TIMEOUT_DRAIN); break; }
       }
     }
-  } else {
+  } else if (warp < 8) {
     // ------------------------------------- softmax group t: tiles n % 2 == t
-    const int t = (warp - 2) >> 2;
+    const int t = warp >> 2;
     const int qw = warp & 3;       // TMEM lane quarter
     const int r = qw * 32 + lane;  // row of the query tile
     const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
@@ -376,40 +472,39 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       const volatile PdTile& dv = ring[n % PD_RING];
       const int flags = dv.flags;
       if (flags & PD_END) break;
-      const int nk = dv.nk, pos = dv.pos, b0 = dv.b0, nrows = dv.nrows, kvh = dv.kvh;
-      const bool active = qw * 32 < nrows;  // (the whole warp)
-      const int b = b0 + r / G;
+      const int nk = dv.nk;
+      const bool active = qw * 32 < dv.nrows;  // (the whole warp)
       if (flags & PD_FIRST_ACC) {
         m_used = -INFINITY;
         l = 0.f;
-        if (a.window >= 0) oldest = r < nrows ? dv.plen + a.lens[b] - 1 - min(a.window, 1 << 30) : 0;
-      }
-      // V rows behind the last key are another sequence's, or older tiles':
-      // they are zeroed (0 * NaN is NaN)
-      if (nk < FA_BN) {
-        if (!mbar_wait_warp(&v_full[t], c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) break;
-        if (r >= nk) zero_tile_row(sV + t * PD_TILE, 16384, r);
-        fence_proxy_async_smem();
+        if (a.window >= 0) oldest = r < dv.nrows ? dv.plen + a.lens[dv.b0 + r / G] - 1 - min(a.window, 1 << 30) : 0;
       }
       if (active) {
         tc_fence_after();
-        uint32_t v[128];
+        const int lo = a.window >= 0 ? oldest - dv.pos : 0;  // the row sees keys lo .. nk-1 of the tile
+        // 32 scores at a time, as far as the tile has keys, twice: for the
+        // maximum, then for P (a whole row of 128 in registers spills, and the L1
+        // beside this much shared memory is too small for that)
+        uint32_t w[32];
+        const auto scores = [&](int k) {
+          tmem_ld_32x32b_x32(lane_addr + s_col + k, w);
+          tmem_ld_wait();
+          if (k + 32 > nk || __any_sync(0xffffffffu, lo > k)) {
+            uint32_t seen = 0xffffffffu;  // bit i: the row sees key k + i
+            if (k + 32 > nk) seen = 0xffffffffu >> (k + 32 - nk);
+            if (lo > k) seen = lo - k < 32 ? seen & (0xffffffffu << (lo - k)) : 0u;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          tmem_ld_32x32b_x32(lane_addr + s_col + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
-        tmem_ld_wait();
-        const int lo = a.window >= 0 ? oldest - pos : 0;  // the row sees keys lo .. nk-1 of the tile
-        if (nk < FA_BN || __any_sync(0xffffffffu, lo > 0)) {
+            for (int i = 0; i < 32; ++i) w[i] = seen & (1u << i) ? w[i] : __float_as_uint(-INFINITY);
+          }
+        };
+        float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int k = 0; k < nk; k += 32) {
+          scores(k);
 #pragma unroll
-          for (int i = 0; i < 128; ++i) v[i] = (i >= lo && i < nk) ? v[i] : __float_as_uint(-INFINITY);
+          for (int i = 0; i < 32; ++i) mp[i & 3] = fmaxf(mp[i & 3], __uint_as_float(w[i]));
         }
-        float mp[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(v[i]);
-#pragma unroll
-        for (int i = 8; i < 128; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
-        const float mx = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                               fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+        const float mx = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])) * sl2;
         // the running max moves only when it grows by more than 8 (base 2)
         const bool grow = mx > m_used + 8.f;
         const float corr = grow ? fast_exp2(m_used - mx) : 1.f;  // 0 when m_used is -inf
@@ -418,20 +513,21 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           m_used = mx;
         }
         const float mu = (m_used == -INFINITY) ? 0.f : m_used;
+        // P as bf16 pairs over the first columns of S, 16 for 32 keys
         float lp[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int hq = 0; hq < 4; ++hq) {  // 32 keys (16 columns of P) at a time
+#pragma unroll 1
+        for (int k = 0; k < nk; k += 32) {
+          if (nk > 32) scores(k);  // (a short tile's are still there)
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const int i = hq * 32 + 2 * e;
-            const float p0 = fast_exp2(fmaf(__uint_as_float(v[i]), sl2, -mu));
-            const float p1 = fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl2, -mu));
+            const float p0 = fast_exp2(fmaf(__uint_as_float(w[2 * e]), sl2, -mu));
+            const float p1 = fast_exp2(fmaf(__uint_as_float(w[2 * e + 1]), sl2, -mu));
             lp[(2 * e) & 3] += p0;
             lp[(2 * e + 1) & 3] += p1;
             pk[e] = pack_bf16(p0, p1);
           }
-          tmem_st_32x32b_x16(lane_addr + s_col + hq * 16, pk);
+          tmem_st_32x32b_x16(lane_addr + s_col + k / 2, pk);
         }
         l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
         if (!(flags & PD_FIRST_ACC) && __any_sync(0xffffffffu, grow)) {
@@ -450,27 +546,38 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
       }
+      // V rows behind the last key, up to its step of 16, are another
+      // sequence's: they are zeroed (0 * NaN is NaN)
+      if (nk & 15) {
+        if (!mbar_wait_warp(&v_full[n % PD_ST], (n / PD_ST) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) break;
+        if (r >= nk && r < ((nk + 15) & ~15)) zero_tile_row(sV + n % PD_ST * PD_TILE, 16384, r);
+        fence_proxy_async_smem();
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[t]);
       if (flags & PD_LAST_ACC) {
         if (active) {
           if (!mbar_wait_warp(&o_done[t], c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) break;
           tc_fence_after();
-          const int odd = flags & PD_ODD ? 1 : 0;
+          // (the tile's entry of the ring stays: its successor's K waits for S
+          // of a tile after this group's next one)
+          const int fl = dv.flags, nrows = dv.nrows, kvh = dv.kvh, b = dv.b0 + r / G;
+          const int odd = fl & PD_ODD ? 1 : 0;
           float* rec;
-          if (flags & PD_CONT)
+          if (fl & PD_CONT)
             rec = a.rec_b + (((long long)cta * a.spt * G + r) * 2 + odd) * PD_REC;
           else
-            rec = a.rec_a + ((((flags & PD_OWN ? 1ll : 0ll) * a.B + b) * a.H + kvh * G + r % G) * 2 + odd) * PD_REC;
+            rec = a.rec_a + ((((fl & PD_OWN ? 1ll : 0ll) * a.B + b) * a.H + kvh * G + r % G) * 2 + odd) * PD_REC;
 #pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t w[32];
-            tmem_ld_32x32b_x32(lane_addr + o_col + k * 32, w);
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[64];
+            tmem_ld_32x32b_x32(lane_addr + o_col + k * 64, *reinterpret_cast<uint32_t(*)[32]>(&w[0]));
+            tmem_ld_32x32b_x32(lane_addr + o_col + k * 64 + 32, *reinterpret_cast<uint32_t(*)[32]>(&w[32]));
             tmem_ld_wait();
             if (r < nrows) {
 #pragma unroll
-              for (int g = 0; g < 8; ++g)
-                *reinterpret_cast<float4*>(rec + k * 32 + g * 4) =
+              for (int g = 0; g < 16; ++g)
+                *reinterpret_cast<float4*>(rec + k * 64 + g * 4) =
                     make_float4(__uint_as_float(w[g * 4]), __uint_as_float(w[g * 4 + 1]),
                                 __uint_as_float(w[g * 4 + 2]), __uint_as_float(w[g * 4 + 3]));
             }
@@ -485,48 +592,53 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == PD_MMA) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
 }
 
-// One warp per (sequence, head) joins its partial results: lane i takes the
-// max and sum of the i-th one, then all lanes add up 4 columns each.
+// One CTA per (sequence, head) joins its partial results, its four warps a
+// quarter of them each: lane i takes the max and sum of the i-th one, then all
+// lanes add up 4 columns each.
 __global__ void __launch_bounds__(128)
     prefix_combine_kernel(const PrefixArgs a, bf16* __restrict__ o, float* __restrict__ lse, int nctas) {
-  const int lane = threadIdx.x & 31;
-  const long long bh = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (bh >= (long long)a.B * a.H) return;
+  __shared__ float s_acc[4][128], s_m[4], s_l[4];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long bh = blockIdx.x;
   const int b = (int)(bh / a.H), h = (int)(bh - (long long)b * a.H);
-  const int G = a.H / a.Hkv, kvh = h / G, W = a.plan[a.B].x;
+  pdl_wait();  // (the partial results)
+  const int G = a.H / a.Hkv, kvh = h / G, U = a.plan[a.B].x;
   const int4 mine = a.plan[b], tile = a.plan[mine.w];
-  // the segments: first tile, tiles, first and last CTA, row in its query tile
-  int f[2], nt[2], c0[2], c1[2], row[2];
-  nt[0] = tile.y;
-  f[0] = tile.x + kvh * nt[0];
-  row[0] = (b - mine.w) * G + h - kvh * G;
-  nt[1] = max(mine.z, 0);
-  f[1] = mine.x + a.Hkv * mine.y + kvh * nt[1];
-  row[1] = h - kvh * G;
-  int count = 0, split = 0;  // partial results; those of the prefix come first
-  for (int s = 0; s < 2; ++s) {
-    c0[s] = nt[s] > 0 ? pd_owner(f[s], nctas, W) : 0;
-    c1[s] = nt[s] > 0 ? pd_owner(f[s] + nt[s] - 1, nctas, W) : -1;
-    if (s == 1) split = count;
-    count += 2 * (c1[s] - c0[s] + 1);
-  }
+  // the two segments: first unit, tiles, first and last CTA, row in its query tile
+  struct Seg {
+    int f, nt, c0, n, row;
+  };
+  const auto seg = [&](int f, int nt, int row) {
+    Seg s{f, nt, 0, 0, row};
+    if (nt > 0) {
+      s.c0 = pd_owner(f, nctas, U);
+      s.n = pd_owner(f + (nt > 1 ? PD_OPEN + PD_UNIT * (nt - 1) : 0), nctas, U) - s.c0 + 1;
+    }
+    return s;
+  };
+  const Seg pre = seg(tile.x + kvh * pd_units(tile.y), tile.y, (b - mine.w) * G + h - kvh * G);
+  const Seg own = seg(mine.x + a.Hkv * pd_units(mine.y) + kvh * pd_units(max(mine.z, 0)), max(mine.z, 0), h - kvh * G);
+  // partial results: two for each CTA of a segment, those of the prefix first
+  int count = 2 * (pre.n + own.n);
   float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
   if (mine.z < 0) count = 0;  // a length outside the cache
-  for (int i0 = 0; i0 < count; i0 += 32) {
-    const int i = i0 + lane;
+  for (int i0 = 0; i0 < count; i0 += 128) {
+    const int i = i0 + lane * 4 + warp;
     const float* rec = nullptr;
     if (i < count) {
-      const int s = i >= split ? 1 : 0, x = i - (s ? split : 0), c = c0[s] + (x >> 1), odd = x & 1;
-      const int from = max(f[s], pd_begin(c, nctas, W)), to = min(f[s] + nt[s], pd_begin(c + 1, nctas, W));
-      if (to - from > odd)  // the odd tiles' result exists if the CTA had two tiles
-        rec = c == c0[s] ? a.rec_a + ((((long long)s * a.B + b) * a.H + h) * 2 + odd) * PD_REC
-                         : a.rec_b + (((long long)c * a.spt * G + row[s]) * 2 + odd) * PD_REC;
+      const bool is_own = i >= 2 * pre.n;
+      const Seg& s = is_own ? own : pre;
+      const int x = i - (is_own ? 2 * pre.n : 0), c = s.c0 + (x >> 1), odd = x & 1;
+      const int j0 = pd_tile(pd_begin(c, nctas, U) - s.f), j1 = min(s.nt, pd_tile(pd_begin(c + 1, nctas, U) - s.f));
+      if (j1 - j0 > odd)  // the odd tiles' result exists if the CTA had two tiles
+        rec = c == s.c0 ? a.rec_a + ((((is_own ? 1ll : 0ll) * a.B + b) * a.H + h) * 2 + odd) * PD_REC
+                        : a.rec_b + (((long long)c * a.spt * G + s.row) * 2 + odd) * PD_REC;
     }
     const float mi = rec ? rec[128] : -INFINITY, li = rec ? rec[129] : 0.f;
     const float mn = fmaxf(m, warp_max(mi));
@@ -537,27 +649,45 @@ __global__ void __launch_bounds__(128)
     m = mn;
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc[k] *= old;
-    const int here = min(32, count - i0);
-#pragma unroll 4
-    for (int j = 0; j < here; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const float* rj = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec), j));
-      if (wj != 0.f) {
-        const float4 u = *reinterpret_cast<const float4*>(rj + lane * 4);
-        acc[0] = fmaf(wj, u.x, acc[0]);
-        acc[1] = fmaf(wj, u.y, acc[1]);
-        acc[2] = fmaf(wj, u.z, acc[2]);
-        acc[3] = fmaf(wj, u.w, acc[3]);
+    const int here = min(32, (count - i0 - warp + 3) / 4);
+    for (int j0 = 0; j0 < here; j0 += 4) {  // four results' loads at a time, before their weights are needed
+      float4 u[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float* rj = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(rec), (j0 + q) & 31));
+        u[q] = rj && j0 + q < here ? *reinterpret_cast<const float4*>(rj + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float wj = __shfl_sync(0xffffffffu, w, (j0 + q) & 31);
+        if (j0 + q < here && wj != 0.f) {
+          acc[0] = fmaf(wj, u[q].x, acc[0]);
+          acc[1] = fmaf(wj, u[q].y, acc[1]);
+          acc[2] = fmaf(wj, u[q].z, acc[2]);
+          acc[3] = fmaf(wj, u[q].w, acc[3]);
+        }
       }
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint2 u;
-  u.x = pack_bf16(acc[0] * inv, acc[1] * inv);
-  u.y = pack_bf16(acc[2] * inv, acc[3] * inv);
-  *reinterpret_cast<uint2*>(o + bh * 128 + lane * 4) = u;
-  if (lane == 0 && lse) lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+  *reinterpret_cast<float4*>(&s_acc[warp][lane * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_l[warp] = l;
+  }
+  __syncthreads();
+  const float mm = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  float sum = 0.f, x = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float w = s_m[q] == -INFINITY ? (s_l[q] == 0.f ? 0.f : 1.f) : fast_exp2(s_m[q] - mm);
+    if (w != 0.f) {
+      sum = fmaf(w, s_l[q], sum);
+      x = fmaf(w, s_acc[q][threadIdx.x], x);
+    }
+  }
+  o[bh * 128 + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+  if (threadIdx.x == 0 && lse) lse[bh] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
 }
 
 }  // namespace gptb
