@@ -1551,7 +1551,7 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
   if (total == 0) return GPTB_OK;  // (empty arrays may have no address)
   if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) || !lse)
     return GPTB_ERR_INVALID_ARG;
-  const long long grid = (long long)((total + FA_QB - 1) / FA_QB) * H;
+  const long long grid = (long long)((total + FA_BM - 1) / FA_BM) * H;
   if (grid > INT_MAX) return GPTB_ERR_UNSUPPORTED;
   if (n_seq == 0) return GPTB_OK;
   if (dev_info().cc_major != 10) return GPTB_ERR_UNSUPPORTED;
@@ -1559,8 +1559,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
   if (!packed_map(&tq, q, H, total, ldq, 128) || !packed_map(&tk, k, Hkv, total, ldk, 128) ||
       !packed_map(&tv, v, Hkv, total, ldv, 128) || !packed_map(&to, o, H, total, ldo, 32))
     return GPTB_ERR_CUDA;
-  TRY(allow_smem(packed_attn_fwd_kernel, FA_SMEM, g_smem_packed_fwd));
-  packed_attn_fwd_kernel<<<(unsigned)grid, FA_THREADS, FA_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(
+  TRY(allow_smem(packed_attn_fwd_kernel, PF_SMEM, g_smem_packed_fwd));
+  packed_attn_fwd_kernel<<<(unsigned)grid, PF_THREADS, PF_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(
       tq, tk, tv, to, static_cast<bf16*>(o), ldo, lse, cu_seqlens, n_seq, total, H, Hkv, window);
   CKL();
   return GPTB_OK;

@@ -58,38 +58,55 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
     *reinterpret_cast<uint4*>(tile + (c >> 3) * half + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
-__global__ void __launch_bounds__(FA_THREADS, 1)
+// Forward.  CTA = 128 consecutive packed rows of one head, two CTAs per SM, 6
+// warps: 0 TMA producer (Q once; K and V tiles of 128 keys, one buffer each:
+// the next K loads during this tile's softmax, the next V during the next
+// tile's), 1 TMEM owner and MMA issuer, 2-5 softmax (thread = query row, its
+// TMEM lane).  S = Q K^T in TMEM columns 0-127, P (bf16 pairs) over its first
+// 64, O in 128-255.  O is rescaled only when a row's running maximum grows by
+// more than 8 in base 2 (P stays below 256 in bf16, and the normalisation uses
+// the same maximum, so the result is exact).
+// The chain S -> softmax -> PV of one CTA leaves the tensor core idle half of
+// the time and its start and end (10 us together) all of it; the other CTA of
+// the SM, at another point of its own work, fills both.  One CTA with two query
+// tiles that share K and V (attention_tc.cuh) has the same steady state and
+// half the K/V reads from L2, but starts and ends alone: one
+// sequence of 8192 rows, 12 heads, took 220 us against 210, 24 ragged ones 84
+// against 73.
+constexpr int PF_THREADS = 192;
+constexpr int PF_SMEM = 1024 + 3 * FA_TILE /*Q, K, V*/;
+
+__global__ void __launch_bounds__(PF_THREADS, 2)
     packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                            bf16* __restrict__ o, long long ldo, float* __restrict__ lse,
                            const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window) {
   extern __shared__ uint8_t fa_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fa_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                // 2 query tiles
-  uint8_t* sK = sQ + 2 * FA_TILE;    // 2 stages
-  uint8_t* sV = sK + 2 * FA_TILE;    // 2 stages
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + 2 * FA_TILE);
+  uint8_t* sQ = smem;
+  uint8_t* sK = sQ + FA_TILE;
+  uint8_t* sV = sK + FA_TILE;
+  __shared__ __align__(8) uint64_t bars[9];
   uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;    // [2 slots]
-  uint64_t* k_empty = bars + 3;   // [2 slots]
-  uint64_t* v_full = bars + 5;    // [2 slots]
-  uint64_t* v_empty = bars + 7;   // [2 slots]
-  uint64_t* s_full = bars + 9;    // [2 query tiles] S_t of the next key tile computed
-  uint64_t* p_full = bars + 11;   // [2 query tiles] P_t written (one arrival per softmax warp)
-  uint64_t* o_done = bars + 13;   // [2 query tiles] O_t += P_t V_j done
-  uint64_t* drain = bars + 15;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 16);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* k_full = bars + 1;
+  uint64_t* k_empty = bars + 2;
+  uint64_t* v_full = bars + 3;
+  uint64_t* v_empty = bars + 4;
+  uint64_t* s_full = bars + 5;
+  uint64_t* p_full = bars + 6;  // one arrival per softmax warp
+  uint64_t* o_done = bars + 7;  // O += P V_j done
+  uint64_t* drain = bars + 8;
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_abort;
+  __shared__ int s_lo;  // first visible row of the tile's first query
+  volatile int* abort_flag = &s_abort;
 
-  __shared__ int s_lo[2];  // first visible row of the first query of each query tile
-
-  // one CTA per (256 consecutive packed rows, head), the last rows first: the
-  // end of a long sequence is its heaviest part
-  const int nqb = (total + FA_QB - 1) / FA_QB;
+  // the last rows first: the end of a long sequence is its heaviest part
+  const int nqb = (total + FA_BM - 1) / FA_BM;
   const int qb = nqb - 1 - (int)blockIdx.x / H;
   const int h = (int)blockIdx.x % H;
   const int kvh = h / (H / Hkv);
-  const int q0 = qb * FA_QB;
+  const int q0 = qb * FA_BM;
   const int n_rows = packed_rows(cu, n_seq, total);
   if (blockIdx.x == 0) packed_check(cu, n_seq, total);
   if (q0 >= n_rows) return;  // (the whole CTA: rows behind the last sequence)
@@ -97,124 +114,82 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 1);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_full[i], 1);
-      mbar_init(&v_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_done[i], 1);
-    }
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    mbar_init(v_full, 1);
+    mbar_init(v_empty, 1);
+    mbar_init(s_full, 1);
+    mbar_init(p_full, 4);
+    mbar_init(o_done, 1);
     mbar_init(drain, 1);
-    *abort_flag = 0;
+    s_abort = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_q);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
-    tma_prefetch_desc(&tm_o);
+    // Q and, under a causal mask always, the last key tile's K need no lookup
+    mbar_arrive_expect_tx(q_full, FA_TILE);
+    tma_load_2d(sQ, &tm_q, q_full, h * 128, q0);
+    tma_load_2d(sQ + 16384, &tm_q, q_full, h * 128 + 64, q0);
   }
+  if (warp == 1) tmem_alloc(&tmem_slot, 256);
   // a softmax thread's query row sees the packed rows kv_lo .. kv_hi
   int tq = 0, kv_lo = 0, kv_hi = -1;
   if (warp >= 2) {
-    tq = q0 + ((warp - 2) >> 2) * FA_BM + (warp & 3) * 32 + lane;
+    tq = q0 + (warp & 3) * 32 + lane;
     if (tq < n_rows) {
       kv_lo = packed_seq(cu, n_seq, tq, n_rows).x;
       if (window >= 0) kv_lo = max(kv_lo, tq - window);
       kv_hi = tq;
     }
-    if ((tq & (FA_BM - 1)) == 0) s_lo[(warp - 2) >> 2] = tq < n_rows ? kv_lo : tq;
+    if (tq == q0) s_lo = kv_lo;
   }
-  if (warp == 1) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  // key tiles that intersect the visible keys of query tile t (none past the
-  // last row); both ranges are monotone in t and overlap or touch, so their
-  // union is one range
-  int lo[2], hi[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int qt = q0 + t * FA_BM;
-    lo[t] = max(s_lo[t], s_lo[0]) / FA_BN;
-    hi[t] = (qt < n_rows) ? min(qt + FA_BM - 1, n_rows - 1) / FA_BN : lo[t] - 1;
-  }
-  const int jlo = lo[0];
-  const int jhi = max(hi[0], hi[1]);
+  const uint32_t tmem = tmem_slot;
+  const int jlo = s_lo / FA_BN, jhi = min(q0 + FA_BM - 1, n_rows - 1) / FA_BN;
+  const int n = jhi - jlo + 1;  // key tiles
 
   if (warp == 0) {
     if (lane == 0) {
-      const int nq = (hi[1] >= lo[1]) ? 2 : 1;
-      mbar_arrive_expect_tx(q_full, nq * FA_TILE);
-      for (int t = 0; t < nq; ++t) {
-        tma_load_2d(sQ + t * FA_TILE, &tm_q, q_full, h * 128, q0 + t * FA_BM);
-        tma_load_2d(sQ + t * FA_TILE + 16384, &tm_q, q_full, h * 128 + 64, q0 + t * FA_BM);
-      }
-      for (int j = jlo; j <= jhi; ++j) {
-        const int i = j - jlo, st = i & 1;
-        const uint32_t par = ((i >> 1) & 1) ^ 1u;
-        const int kr = j * FA_BN;
-        if (!mbar_wait(&k_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&k_full[st], FA_TILE);
-        uint8_t* k = sK + st * FA_TILE;
-        tma_load_2d(k, &tm_k, &k_full[st], kvh * 128, kr);
-        tma_load_2d(k + 16384, &tm_k, &k_full[st], kvh * 128 + 64, kr);
-        if (!mbar_wait(&v_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(&v_full[st], FA_TILE);
-        uint8_t* v = sV + st * FA_TILE;
-        tma_load_2d(v, &tm_v, &v_full[st], kvh * 128, kr);
-        tma_load_2d(v + 16384, &tm_v, &v_full[st], kvh * 128 + 64, kr);
+      for (int i = 0; i < n; ++i) {
+        const uint32_t par = (i & 1) ^ 1u;
+        const int kr = (jlo + i) * FA_BN;
+        if (!mbar_wait(k_empty, par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(k_full, FA_TILE);
+        tma_load_2d(sK, &tm_k, k_full, kvh * 128, kr);
+        tma_load_2d(sK + 16384, &tm_k, k_full, kvh * 128 + 64, kr);
+        if (!mbar_wait(v_empty, par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(v_full, FA_TILE);
+        tma_load_2d(sV, &tm_v, v_full, kvh * 128, kr);
+        tma_load_2d(sV + 16384, &tm_v, v_full, kvh * 128 + 64, kr);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t IDESC_S = make_idesc(128, 128, false, false, false);
       constexpr uint32_t IDESC_O = make_idesc(128, 128, false, true, false);
+      const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
       bool ok = mbar_wait(q_full, 0, abort_flag, ERRW_TIMEOUT_MMA);
-      auto in = [&](int t, int j) { return j >= lo[t] && j <= hi[t]; };
-      // S_t for key tile j; the K slot is released after its last score product
-      auto issue_s = [&](int t, int j) -> bool {
-        const int i = j - jlo, st = i & 1;
-        if (!mbar_wait(&k_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
-        tc_fence_after();
-        const uint32_t aQ = smem_u32(sQ + t * FA_TILE), aK = smem_u32(sK + st * FA_TILE);
+      for (int i = 0; ok && i <= n; ++i) {
+        if (i > 0) {  // O += P V of the tile before, P read from TMEM
+          if (!mbar_wait(v_full, (i - 1) & 1, abort_flag, ERRW_TIMEOUT_MMA) ||
+              !mbar_wait(p_full, (i - 1) & 1, abort_flag, ERRW_TIMEOUT_MMA))
+            break;
+          tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ss(tmem + t * 128, fa_desc_k(aQ, k), fa_desc_k(aK, k), IDESC_S, k > 0 ? 1u : 0u);
-        mma_commit(&s_full[t]);
-        if (t == 1 || !in(1, j)) mma_commit(&k_empty[st]);
-        return true;
-      };
-      // O_t += P_t V_j once the softmax has written P_t; the V slot is released after its last PV product
-      auto issue_pv = [&](int t, int j) -> bool {
-        const int i = j - jlo, st = i & 1;
-        const int c = j - lo[t];
-        if (!mbar_wait(&v_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
-        if (!mbar_wait(&p_full[t], c & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
-        tc_fence_after();
-        const uint32_t aV = smem_u32(sV + st * FA_TILE);
-        // A = P_t from TMEM (lane = query row, 8 columns per 16 keys)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, fa_desc_mn(aV, k), IDESC_O,
-                      (c > 0 || k > 0) ? 1u : 0u);
-        mma_commit(&o_done[t]);
-        if (t == 1 || !in(1, j)) mma_commit(&v_empty[st]);
-        return true;
-      };
-      if (ok && in(0, jlo)) ok = issue_s(0, jlo);
-      if (ok && in(1, jlo)) ok = issue_s(1, jlo);
-      for (int j = jlo; ok && j <= jhi; ++j) {
-        if (in(0, j)) {
-          ok = issue_pv(0, j) && (j + 1 > hi[0] || issue_s(0, j + 1));
-          if (!ok) break;
+          for (int k = 0; k < 8; ++k)
+            mma_bf16_ts(tmem + 128, tmem + k * 8, fa_desc_mn(aV, k), IDESC_O, (i > 1 || k > 0) ? 1u : 0u);
+          mma_commit(v_empty);
+          mma_commit(o_done);
         }
-        // (the second query tile may begin many key tiles after the first: a
-        // sequence that ends between them.  Its first S waits for its turn, as
-        // the K ring holds two tiles.)
-        if (in(1, j) && !issue_pv(1, j)) break;
-        if (in(1, j + 1)) ok = issue_s(1, j + 1);
+        if (i == n) break;
+        // S: products of one thread run in order, so it overwrites P after the
+        // product that reads it
+        if (!mbar_wait(k_full, i & 1, abort_flag, ERRW_TIMEOUT_MMA)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_bf16_ss(tmem, fa_desc_k(aQ, k), fa_desc_k(aK, k), IDESC_S, k > 0 ? 1u : 0u);
+        mma_commit(s_full);
+        mma_commit(k_empty);
       }
       if (*abort_flag) {
         mma_commit(drain);
@@ -224,32 +199,25 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
       }
     }
   } else {
-    // softmax of query tile tt: TMEM lane quarter qw = warp % 4 -> rows 32*qw .. 32*qw+31
-    const int tt = (warp - 2) >> 2;
-    const int qw = warp & 3;
-    const int r = qw * 32 + lane;        // row within the query tile
+    const int qw = warp & 3;       // TMEM lane quarter
+    const int r = qw * 32 + lane;  // row within the query tile
     const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
-    const uint32_t s_col = (uint32_t)(tt * 128), o_col = (uint32_t)(256 + tt * 128);
     const float sl2 = LOG2E / sqrtf(128.f);
-    const int qt0 = q0 + tt * FA_BM;  // first query of the tile
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    const int lo_t = tt ? lo[1] : lo[0];
-    const int n = (tt ? hi[1] : hi[0]) - lo_t + 1;  // key tiles of this query tile (0 past the last row)
     for (int c = 0; c < n && ok; ++c) {
-      const int k0 = (lo_t + c) * FA_BN;
-      ok = mbar_wait_warp(&s_full[tt], c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      const int k0 = (jlo + c) * FA_BN;
+      ok = mbar_wait_warp(s_full, c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
       if (!ok) break;
       tc_fence_after();
       uint32_t v[128];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        tmem_ld_32x32b_x32(lane_addr + s_col + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
+        tmem_ld_32x32b_x32(lane_addr + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
       tmem_ld_wait();
       // rows are masked in a tile that reaches past the first query, or
       // before what the last one sees (kv_lo grows with the row)
-      const bool need_mask = __any_sync(0xffffffffu, k0 < kv_lo || k0 + FA_BN - 1 > kv_hi);
-      if (need_mask) {
+      if (__any_sync(0xffffffffu, k0 < kv_lo || k0 + FA_BN - 1 > kv_hi)) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) {
           const int jk = k0 + i;
@@ -272,7 +240,7 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
       }
       const float mu = (m_used == -INFINITY) ? 0.f : m_used;
       // P = exp2(s*scale - m) as bf16 pairs (key 2c in the low half) over the
-      // first 64 columns of S_t
+      // first 64 columns of S
       float lp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int hq = 0; hq < 4; ++hq) {  // 32 keys (16 columns of P) at a time
@@ -286,60 +254,55 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
           lp[(2 * e + 1) & 3] += p1;
           pk[e] = pack_bf16(p0, p1);
         }
-        tmem_st_32x32b_x16(lane_addr + s_col + hq * 16, pk);
+        tmem_st_32x32b_x16(lane_addr + hq * 16, pk);
       }
       l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
       // V rows behind the last sequence may hold anything (0 * NaN is NaN):
-      // they are zeroed before the product that reads them.  Both groups write
-      // the same zeros.
-      if (n_rows < total && k0 + FA_BN > n_rows && c == n - 1) {
-        const int i = lo_t + c - jlo;
-        ok = mbar_wait_warp(&v_full[i & 1], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      // they are zeroed before the product that reads them
+      if (n_rows < total && k0 + FA_BN > n_rows) {
+        ok = mbar_wait_warp(v_full, c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
-        if (k0 + r >= n_rows) zero_tile_row(sV + (i & 1) * FA_TILE, 16384, r);
+        if (k0 + r >= n_rows) zero_tile_row(sV, 16384, r);
         fence_proxy_async_smem();
       }
-      // O_t to the new max (the TMEM accesses are warp-collective: the whole
-      // warp enters, rows that keep their max use 1).  O_t holds every PV
-      // product up to key tile c-1 (the commit of S_t above follows them);
-      // the wait states it.
+      // O to the new max (the TMEM accesses are warp-collective: the whole
+      // warp enters, rows that keep their max use 1).  O holds every PV product
+      // up to tile c-1 (the commit of S above follows them); the wait states it.
       if (c > 0 && __any_sync(0xffffffffu, grow)) {
-        ok = mbar_wait_warp(&o_done[tt], (c - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+        ok = mbar_wait_warp(o_done, (c - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < 4; ++k) {
           uint32_t w[32];
-          tmem_ld_32x32b_x32(lane_addr + o_col + k * 32, w);
+          tmem_ld_32x32b_x32(lane_addr + 128 + k * 32, w);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * corr);
-          tmem_st_32x32b_x32(lane_addr + o_col + k * 32, w);
+          tmem_st_32x32b_x32(lane_addr + 128 + k * 32, w);
         }
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[tt]);
+      if (lane == 0) mbar_arrive(p_full);
     }
-    if (n > 0 && __all_sync(0xffffffffu, ok) &&
-        mbar_wait_warp(&o_done[tt], (n - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
+    if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(o_done, (n - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      // O_t (bf16) leaves through the Q_t tile, free once every S_t product
-      // has completed (they precede the last PV_t that o_done follows): two
-      // 64-column halves of 128 rows x 128 bytes, 128-byte swizzle; a warp
-      // whose 32 rows all lie inside the sequences stores them with two TMA
-      // boxes, the last rows go out one by one
-      uint8_t* stg = sQ + tt * FA_TILE;
-      const int row0 = qt0 + qw * 32;  // first query of this warp's rows
+      // O (bf16) leaves through the Q tile, free once every S product has
+      // completed (they precede the last PV that o_done follows): two 64-column
+      // halves of 128 rows x 128 bytes, 128-byte swizzle; a warp whose 32 rows
+      // all lie inside the sequences stores them with two TMA boxes, the last
+      // rows go out one by one
+      const int row0 = q0 + qw * 32;  // first query of this warp's rows
       const bool whole = row0 + 32 <= n_rows;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // columns 32k .. 32k+31
         uint32_t w[32];
-        tmem_ld_32x32b_x32(lane_addr + o_col + k * 32, w);
+        tmem_ld_32x32b_x32(lane_addr + 128 + k * 32, w);
         tmem_ld_wait();
-        uint8_t* row = stg + (k >> 1) * 16384 + r * 128;
+        uint8_t* row = sQ + (k >> 1) * 16384 + r * 128;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint4 u;
@@ -357,8 +320,8 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && whole) {
-        tma_store_2d(&tm_o, stg + qw * 4096, h * 128, row0);
-        tma_store_2d(&tm_o, stg + 16384 + qw * 4096, h * 128 + 64, row0);
+        tma_store_2d(&tm_o, sQ + qw * 4096, h * 128, row0);
+        tma_store_2d(&tm_o, sQ + 16384 + qw * 4096, h * 128 + 64, row0);
         bulk_commit_group();
         bulk_wait_read0();  // the tile's shared memory is read before the CTA ends
       }
@@ -370,10 +333,9 @@ __global__ void __launch_bounds__(FA_THREADS, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
 }
-
 
 // Roles, TMEM columns and barriers as in attn_bwd_tc_kernel.
 __global__ void __launch_bounds__(AB2_THREADS, 1)
