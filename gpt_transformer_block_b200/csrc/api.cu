@@ -209,6 +209,23 @@ int allow_smem(K kernel, int bytes, SmemOnce& once) {
 }
 SmemOnce g_smem_packed_fwd, g_smem_packed_bwd, g_smem_prefix;
 
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cs, cudaStream_t st,
+                           A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cs;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cs > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // a kernel that begins with pdl_wait(), set up while the one before it in the stream ends
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... args) {
@@ -1534,7 +1551,7 @@ bool packed_ok(const void* p, long long ld, int heads) {
   return p && aligned16(p) && ld % 8 == 0 && ld >= (long long)heads * 128 && ld < (1ll << 36);
 }
 bool packed_shape_ok(const int32_t* cu, int total, int n_seq, int H, int Hkv, int window) {
-  return cu && total >= 0 && total <= (1 << 30) && n_seq >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 && H <= (1 << 16) &&
+  return cu && total >= 0 && total <= (1 << 30) && n_seq >= 0 && n_seq <= (1 << 26) && H > 0 && Hkv > 0 && H % Hkv == 0 && H <= (1 << 16) &&
          window >= -1;
 }
 bool packed_map(CUtensorMap* m, const void* p, int heads, int total, long long ld, int box_rows) {
@@ -1597,13 +1614,21 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
     return GPTB_ERR_CUDA;
   const long long sms = dev_info().sms;
   const auto blocks = [&](long long n) { return (int)std::max(1ll, std::min((n + 255) / 256, sms * 8)); };
-  packed_attn_pre_kernel<<<blocks((long long)total * H * 32), 256, 0, st>>>(
-      static_cast<const bf16*>(o), ldo, static_cast<const bf16*>(dout), lddo, D, acc, cu_seqlens, n_seq, total, H);
+  const int rows = (int)std::max(1ll, std::min<long long>(PB_PRE_ROWS, total / (sms * 4)));  // of a CTA; few for a short batch
+  const long long few = (window >= 0 && window < PB_FEW ? total : std::min<long long>(total, (long long)n_seq * PB_FEW)) * (long long)H;
+  const int few_ctas = (int)std::min((few + 7) / 8, sms * 8);
+  packed_attn_pre_kernel<<<few_ctas + (total + rows - 1) / rows, 256, 0, st>>>(
+      static_cast<const bf16*>(q), ldq, static_cast<const bf16*>(k), ldk, static_cast<const bf16*>(v), ldv,
+      static_cast<const bf16*>(o), ldo, static_cast<const bf16*>(dout), lddo, lse, D, acc, cu_seqlens, n_seq, total, H,
+      Hkv, window, rows, few_ctas);
   CKL();
   TRY(allow_smem(packed_attn_bwd_kernel, AB2_SMEM, g_smem_packed_bwd));
-  packed_attn_bwd_kernel<<<(unsigned)grid, AB2_THREADS, AB2_SMEM, st>>>(
-      tq, tk, tv, tdo, tdk, tdv, static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, lse, D, acc, cu_seqlens,
-      n_seq, total, H, Hkv, window);
+  // CTAs per chain of steps: as many as the SMs have room for at once
+  int cs = 1;
+  while (cs < PB_CLUSTER && grid * cs * 2 <= sms) cs *= 2;
+  CK(launch_cluster(packed_attn_bwd_kernel, (unsigned)(grid * cs), AB2_THREADS, AB2_SMEM, cs, st, tq, tk, tv, tdo, tdk, tdv,
+                    static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, lse, D, acc, cu_seqlens, n_seq, total, H,
+                    Hkv, window, cs));
   CKL();
   packed_attn_dq_kernel<<<blocks((long long)total * H * 16), 256, 0, st>>>(acc, static_cast<bf16*>(dq), lddq, cu_seqlens,
                                                                            n_seq, total, H);
@@ -1733,18 +1758,7 @@ int policy_rows(const T* z, T* dz, PolicyArgs a, int* parts, cudaStream_t st) {
   const long long fill = std::min(ctas / a.rows, row / (2 * POL_THREADS));
   a.cs = (int)std::min<long long>(POL_CLUSTER, std::max(hold, fill));
   *parts = (int)std::max(1ll, std::min<long long>(a.rows, std::min<long long>(POL_MAX_PARTS, ctas / a.cs)));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(*parts * a.cs));
-  cfg.blockDim = dim3(POL_THREADS);
-  cfg.dynamicSmemBytes = POL_SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)a.cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  CK(cudaLaunchKernelEx(&cfg, policy_rows_kernel<T, ALIGNED>, z, dz, a));
+  CK(launch_cluster(policy_rows_kernel<T, ALIGNED>, (unsigned)(*parts * a.cs), POL_THREADS, POL_SMEM, a.cs, st, z, dz, a));
   CKL();
   return GPTB_OK;
 }

@@ -337,14 +337,21 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   }
 }
 
-// Roles, TMEM columns and barriers as in attn_bwd_tc_kernel.
+// Backward.  Roles, TMEM columns and barriers as in attn_bwd_tc_kernel: 128
+// keys of one kv head per CTA, a chain of steps of one query head and 64
+// queries each.  A chain costs 10 us to start and end and 2 us per step, so
+// where there are fewer chains than SMs a cluster of up to 8 CTAs shares each:
+// every CTA takes a part of its steps, and the partial dK and dV meet through
+// distributed shared memory, added in a fixed order (5 sequences of 12 to 180
+// tokens, 8 query heads over 2: CLUSTER_NOTE).
+constexpr int PB_CLUSTER = 8;
 __global__ void __launch_bounds__(AB2_THREADS, 1)
     packed_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
                            const __grid_constant__ CUtensorMap tm_dk, const __grid_constant__ CUtensorMap tm_dv,
                            bf16* __restrict__ dk, long long lddk, bf16* __restrict__ dv, long long lddv,
                            const float* __restrict__ lse, const float* __restrict__ Dd, float* __restrict__ dq,
-                           const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window) {
+                           const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window, int cs) {
   extern __shared__ uint8_t ab_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ab_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sK = smem;
@@ -370,7 +377,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
 
   __shared__ int s_vis[2];  // last query that sees the tile's first key; ... its last key
 
-  const int kb = (int)blockIdx.x / Hkv, kvh = (int)blockIdx.x % Hkv;
+  const int rank = (int)blockIdx.x % cs, chain = (int)blockIdx.x / cs;
+  const int kb = chain / Hkv, kvh = chain % Hkv;
   const int G = H / Hkv;
   const int k0 = kb * AB2_BK;
   const int n_rows = packed_rows(cu, n_seq, total);
@@ -420,7 +428,9 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
   const int q_first = s_vis[0];
   const int qt_lo = k0 / AB2_BQ;
   const int nq = s_vis[1] / AB2_BQ - qt_lo + 1;
-  const int steps = G * nq;
+  // this CTA's steps: first .. first + steps - 1 of the chain's
+  const int first = (int)((long long)G * nq * rank / cs);
+  const int steps = (int)((long long)G * nq * (rank + 1) / cs) - first;
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -434,8 +444,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
     bool ok = true;
     for (int i = 0; i < steps && ok; ++i) {
       const int st = i % AB2_STAGES;
-      const int hh = kvh * G + i / nq;
-      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      const int hh = kvh * G + (first + i) / nq;
+      const int q0 = (qt_lo + (first + i) % nq) * AB2_BQ;
       ok = mbar_wait_warp(&qdo_empty[st], ((i / AB2_STAGES) & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_PRODUCER);
       if (!ok) break;
       // the tile loads go out first; LSE and D (plain loads, guarded at the
@@ -510,7 +520,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
         if (i > 0 && !grads(i - 1)) { ok = false; break; }
       }
       if (ok && steps > 0) ok = grads(steps - 1);
-      mma_commit(acc_done);
+      if (ok && steps == 0) mbar_arrive(acc_done);  // (nothing to wait for)
+      else mma_commit(acc_done);
       if (*abort_flag) {
         mma_commit(drain);
         const unsigned long long t0 = globaltimer_ns();
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
     bool ok = true;
     for (int i = 0; i < steps && ok; ++i) {
       const int st = i % AB2_STAGES;
-      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      const int q0 = (qt_lo + (first + i) % nq) * AB2_BQ;
       ok = mbar_wait_warp(s_full, i & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
       if (!ok) break;
       tc_fence_after();
@@ -612,6 +623,17 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
         tmem_ld_32x32b_x32(lane_addr + which * 128 + cb * 64, v0);
         tmem_ld_32x32b_x32(lane_addr + which * 128 + cb * 64 + 32, v1);
         tmem_ld_wait();
+        if (cs > 1) {  // this CTA's part in fp32 (0 without a step): rows of 32 16-byte chunks, chunk c at c ^ (row % 32)
+          float4* prow = reinterpret_cast<float4*>(sQ) + (which * 128 + r) * 32;
+#pragma unroll
+          for (int g = 0; g < 16; ++g) {
+            const uint32_t* w = g < 8 ? v0 + g * 4 : v1 + (g - 8) * 4;
+            prow[(cb * 16 + g) ^ lane] =
+                steps > 0 ? make_float4(__uint_as_float(w[0]), __uint_as_float(w[1]), __uint_as_float(w[2]), __uint_as_float(w[3]))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          continue;
+        }
         uint8_t* prow = stg + which * 4096 + lane * 128;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {  // 16-byte chunk g: columns 8g .. 8g+7
@@ -632,7 +654,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && whole) {
+      if (lane == 0 && whole && cs == 1) {
         tma_store_2d(&tm_dk, stg, kvh * 128 + cb * 64, k0 + qw * 32);
         tma_store_2d(&tm_dv, stg + 4096, kvh * 128 + cb * 64, k0 + qw * 32);
         bulk_commit_group();
@@ -652,8 +674,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
     bool ok = true;
     for (int i = 0; i < steps; ++i) {
-      const int hh = kvh * G + i / nq;
-      const int q0 = (qt_lo + i % nq) * AB2_BQ;
+      const int hh = kvh * G + (first + i) / nq;
+      const int q0 = (qt_lo + (first + i) % nq) * AB2_BQ;
       ok = ok && mbar_wait_warp(dq_full, i & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
       uint32_t v0[32];
       if (ok) {
@@ -690,6 +712,33 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
       }
     }
   }
+  if (cs > 1) {
+    // the parts of the cluster's CTAs, added in their order: CTA `rank` does its
+    // share of the rows, 8 columns at a time
+    __syncwarp();
+    cluster_sync_all();
+    const int rows = AB2_BK / cs;
+    for (int x = threadIdx.x; x < 2 * rows * 16; x += AB2_THREADS) {
+      const int which = x / (rows * 16), rr = rank * rows + x / 16 % rows, c = (x & 15) * 2;
+      float s[8] = {};
+      for (int q = 0; q < cs; ++q) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float4 w;
+          const uint32_t at = map_shared_rank(reinterpret_cast<float4*>(sQ) + (which * 128 + rr) * 32 + ((c + half) ^ (rr & 31)), q);
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(w.x), "=f"(w.y), "=f"(w.z), "=f"(w.w)
+                       : "r"(at) : "memory");
+          s[half * 4 + 0] += w.x;
+          s[half * 4 + 1] += w.y;
+          s[half * 4 + 2] += w.z;
+          s[half * 4 + 3] += w.w;
+        }
+      }
+      if (k0 + rr < n_rows)
+        store8((which ? dv + (long long)(k0 + rr) * lddv : dk + (long long)(k0 + rr) * lddk) + kvh * 128 + c * 4, s);
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its part
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -698,32 +747,108 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
   }
 }
 
-// before the backward: D = rowsum(dO o) of each (row, head) and the fp32 dQ
-// sums set to 0, one warp per (row, head), 4 columns per lane
+// Before the backward: D = rowsum(dO o) of each (row, head) and the fp32 dQ
+// sums set to 0, a warp per (row, head) pair, 4 columns per lane; bound by HBM (8
+// bytes per element).  o has been rounded to bf16, which moves dS = P (dP - D)
+// by P dO (o rounded - o): next to what rounding dS to bf16 costs this is
+// 1 / sqrt(visible keys).  So for rows that see at most PB_FEW keys D is taken
+// as the sum of P dP, which needs no o: two lanes per key, by CTAs of their own.  (Without it dq and
+// dk of 5 sequences of 12 to 180 tokens were 2.6e-3 off in the norm, with it
+// FEW_NOTE; 1.7e-3 is the rounding of the result alone.)
+constexpr int PB_FEW = 16;
+constexpr int PB_PRE_ROWS = 16;  // most rows of a CTA
+
+// sum over 64 columns of two bf16 rows
+__device__ __forceinline__ float dot64(const bf16* __restrict__ x, const bf16* __restrict__ y) {
+  float s = 0.f;
+#pragma unroll
+  for (int c = 0; c < 64; c += 8) {
+    float a[8], b[8];
+    load8(x + c, a);
+    load8(y + c, b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(a[k], b[k], s);
+  }
+  return s;
+}
+
 __global__ void __launch_bounds__(256)
-    packed_attn_pre_kernel(const bf16* __restrict__ o, long long ldo, const bf16* __restrict__ dO, long long lddo,
+    packed_attn_pre_kernel(const bf16* __restrict__ q, long long ldq, const bf16* __restrict__ k, long long ldk,
+                           const bf16* __restrict__ v, long long ldv, const bf16* __restrict__ o, long long ldo,
+                           const bf16* __restrict__ dO, long long lddo, const float* __restrict__ lse,
                            float* __restrict__ D, float* __restrict__ dq, const int32_t* __restrict__ cu, int n_seq,
-                           int total, int H) {
+                           int total, int H, int Hkv, int window, int rows, int few_ctas) {
+  __shared__ int s_first[PB_PRE_ROWS];  // first visible row of each of the CTA's rows
   const int n_rows = packed_rows(cu, n_seq, total);
   if (blockIdx.x == 0) packed_check(cu, n_seq, total);
-  const long long nw = (long long)n_rows * H;
-  const int lane = threadIdx.x & 31;
-  for (long long w = (blockIdx.x * (long long)blockDim.x + threadIdx.x) >> 5; w < nw;
-       w += ((long long)gridDim.x * blockDim.x) >> 5) {
-    const long long t = w / H;
-    const int h = (int)(w - t * H);
-    const uint2 a = *reinterpret_cast<const uint2*>(o + t * ldo + h * 128 + lane * 4);
-    const uint2 b = *reinterpret_cast<const uint2*>(dO + t * lddo + h * 128 + lane * 4);
-    const __nv_bfloat162 *ha = reinterpret_cast<const __nv_bfloat162*>(&a), *hb = reinterpret_cast<const __nv_bfloat162*>(&b);
-    float acc = 0.f;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float2 x = __bfloat1622float2(ha[k]), y = __bfloat1622float2(hb[k]);
-      acc = fmaf(x.x, y.x, fmaf(x.y, y.y, acc));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int STEP = 8, AHEAD = 4;
+  if ((int)blockIdx.x < few_ctas) {
+    // the rows that see few keys: the first ones of every sequence, or all
+    const bool every = window >= 0 && window < PB_FEW;
+    const long long items = (every ? (long long)n_rows : (long long)n_seq * PB_FEW) * H;
+#pragma unroll 1
+    for (long long i = (long long)blockIdx.x * STEP + warp; i < items; i += (long long)few_ctas * STEP) {
+      const int x = (int)(i / H), h = (int)(i - (long long)x * H);
+      int t, first;
+      if (every) {
+        t = x;
+        first = max(packed_seq(cu, n_seq, t, n_rows).x, t - window);
+      } else {
+        first = cu[x / PB_FEW];
+        if (first < 0 || first >= n_rows) continue;  // (an empty sequence at the end; bad offsets)
+        t = first + x % PB_FEW;
+        if (t >= min(cu[x / PB_FEW + 1], n_rows)) continue;
+      }
+      const int j = first + (lane >> 1), c = (lane & 1) * 64, kvh = h / (H / Hkv);
+      float acc = 0.f;
+      if (j <= t) {
+        float s = dot64(q + t * ldq + h * 128 + c, k + j * ldk + kvh * 128 + c);
+        float dp = dot64(dO + t * lddo + h * 128 + c, v + j * ldv + kvh * 128 + c);
+        const unsigned both = 3u << (lane & 30);
+        s += __shfl_xor_sync(both, s, 1);
+        dp += __shfl_xor_sync(both, dp, 1);
+        acc = (lane & 1) ? 0.f
+                         : fast_exp2(fmaf(s, LOG2E * rsqrtf(128.f), -lse[(long long)h * total + t] * LOG2E)) * dp;
+      }
+      acc = warp_sum(acc);
+      if (lane == 0) D[(long long)h * total + t] = acc;
     }
-    acc = warp_sum(acc);
-    if (lane == 0) D[(long long)h * total + t] = acc;
-    *reinterpret_cast<float4*>(dq + w * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    return;
+  }
+  const int r0 = ((int)blockIdx.x - few_ctas) * rows;
+  if (r0 >= n_rows) return;
+  if (threadIdx.x < rows && r0 + (int)threadIdx.x < n_rows) {
+    const int t = r0 + threadIdx.x, first = packed_seq(cu, n_seq, t, n_rows).x;
+    s_first[threadIdx.x] = window >= 0 ? max(first, t - min(window, t)) : first;
+  }
+  __syncthreads();
+  const int n = min(rows, n_rows - r0) * H;  // (row, head) pairs, dealt out to the warps
+  for (int i0 = warp; i0 < n; i0 += STEP * AHEAD) {
+    uint2 a[AHEAD], b[AHEAD];
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int i = i0 + x * STEP;
+      if (i >= n) break;
+      const int t = r0 + i / H, h = i % H;
+      a[x] = *reinterpret_cast<const uint2*>(o + (long long)t * ldo + h * 128 + lane * 4);
+      b[x] = *reinterpret_cast<const uint2*>(dO + (long long)t * lddo + h * 128 + lane * 4);
+      *reinterpret_cast<float4*>(dq + ((long long)t * H + h) * 128 + lane * 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int x = 0; x < AHEAD; ++x) {
+      const int i = i0 + x * STEP;
+      if (i >= n) break;
+      const __nv_bfloat162 *ha = reinterpret_cast<const __nv_bfloat162*>(&a[x]), *hb = reinterpret_cast<const __nv_bfloat162*>(&b[x]);
+      float acc = 0.f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 u = __bfloat1622float2(ha[k]), w = __bfloat1622float2(hb[k]);
+        acc = fmaf(u.x, w.x, fmaf(u.y, w.y, acc));
+      }
+      acc = warp_sum(acc);
+      if (lane == 0 && r0 + i / H - s_first[i / H] >= PB_FEW) D[(long long)(i % H) * total + r0 + i / H] = acc;
+    }
   }
 }
 

@@ -84,6 +84,22 @@ def test_rows_behind_the_last_sequence_hold_nan_and_stay(cuda_lib, lens, pad):
     check(got, want, m, 2, 1)
 
 
+@pytest.mark.parametrize("lens", [[700, 13, 257, 40, 1400], [60] * 40])
+def test_packed_more_chains_than_multiprocessors(cuda_lib, lens):
+    """19 tiles of 6 kv heads: each chain of backward steps by one CTA (a cluster shares each where there are fewer)."""
+    got, want, m = run(cuda_lib, lens, 6, 6, -1)
+    check(got, want, m, 6, 6)
+
+
+@pytest.mark.parametrize("H,Hk,n", [(8, 8, 1), (8, 2, 500), (1, 1, 900), (16, 1, 130)])
+def test_packed_chains_shared_by_clusters(cuda_lib, H, Hk, n):
+    """Clusters of 8, 4 and 8 CTAs, some of them without a step; two calls give the same dk and dv bits."""
+    a, want, m = run(cuda_lib, [n, 3], H, Hk, -1, seed=n)
+    check(a, want, m, H, Hk)
+    b, _, _ = run(cuda_lib, [n, 3], H, Hk, -1, seed=n)
+    assert torch.equal(a["dk"], b["dk"]) and torch.equal(a["dv"], b["dv"])
+
+
 def test_packed_long_sequence_with_window(cuda_lib):
     got, want, m = run(cuda_lib, [1500, 900], 2, 2, 300)
     check(got, want, m, 2, 2)
