@@ -1573,8 +1573,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
   if (n_seq == 0) return GPTB_OK;
   if (dev_info().cc_major != 10) return GPTB_ERR_UNSUPPORTED;
   CUtensorMap tq, tk, tv, to;
-  if (!packed_map(&tq, q, H, total, ldq, 128) || !packed_map(&tk, k, Hkv, total, ldk, 128) ||
-      !packed_map(&tv, v, Hkv, total, ldv, 128) || !packed_map(&to, o, H, total, ldo, 32))
+  if (!packed_map(&tq, q, H, total, ldq, 128) || !packed_map(&tk, k, Hkv, total, ldk, PF_BN) ||
+      !packed_map(&tv, v, Hkv, total, ldv, PF_BN) || !packed_map(&to, o, H, total, ldo, 32))
     return GPTB_ERR_CUDA;
   TRY(allow_smem(packed_attn_fwd_kernel, PF_SMEM, g_smem_packed_fwd));
   packed_attn_fwd_kernel<<<(unsigned)grid, PF_THREADS, PF_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(

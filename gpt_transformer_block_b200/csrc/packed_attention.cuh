@@ -59,22 +59,24 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
 }
 
 // Forward.  CTA = 128 consecutive packed rows of one head, two CTAs per SM, 6
-// warps: 0 TMA producer (Q once; K and V tiles of 128 keys, one buffer each:
-// the next K loads during this tile's softmax, the next V during the next
-// tile's), 1 TMEM owner and MMA issuer, 2-5 softmax (thread = query row, its
-// TMEM lane).  S = Q K^T in TMEM columns 0-127, P (bf16 pairs) over its first
-// 64, O in 128-255.  O is rescaled only when a row's running maximum grows by
-// more than 8 in base 2 (P stays below 256 in bf16, and the normalisation uses
-// the same maximum, so the result is exact).
-// The chain S -> softmax -> PV of one CTA leaves the tensor core idle half of
-// the time and its start and end (10 us together) all of it; the other CTA of
-// the SM, at another point of its own work, fills both.  One CTA with two query
-// tiles that share K and V (attention_tc.cuh) has the same steady state and
-// half the K/V reads from L2, but starts and ends alone: one
-// sequence of 8192 rows, 12 heads, took 220 us against 210, 24 ragged ones 84
-// against 73.
+// warps: 0 TMA producer (Q once; K and V tiles of 64 keys, two stages each), 1
+// TMEM owner and MMA issuer, 2-5 softmax (thread = query row, its TMEM lane).
+// S = Q K^T of tile i in TMEM columns 64 (i % 2) .., P (bf16 pairs) over the
+// first half of it, O in columns 128-255.  The products of one thread run in
+// order, S of tile i+1 is issued before PV of tile i, so the softmax warps find
+// the next scores ready and the tensor core works while they do; the next S but
+// one overwrites P after the product that reads it.  O is rescaled only when a
+// row's running maximum grows by more than 8 in base 2 (P stays below 256 in
+// bf16, and the normalisation uses the same maximum, so the result is exact).
+// What bounds it: the softmax (its exponentials alone take half of the time on
+// their unit), and the start and end of a CTA, which the other CTA of the SM
+// fills.  One sequence of 8192 rows, 12 heads: FWD_NOTE us; with 128-key tiles
+// and so no room for a second S 204, as one CTA of two query tiles per SM
+// (attention_tc.cuh) 220.
 constexpr int PF_THREADS = 192;
-constexpr int PF_SMEM = 1024 + 3 * FA_TILE /*Q, K, V*/;
+constexpr int PF_BN = 64;
+constexpr int PF_KV = PF_BN * 128 * 2;                     // one K or V tile: two 64-column swizzled halves of 8 KB
+constexpr int PF_SMEM = 1024 + FA_TILE /*Q*/ + 4 * PF_KV;  // K, V x2
 
 __global__ void __launch_bounds__(PF_THREADS, 2)
     packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -84,18 +86,18 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   extern __shared__ uint8_t fa_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fa_smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sK = sQ + FA_TILE;
-  uint8_t* sV = sK + FA_TILE;
-  __shared__ __align__(8) uint64_t bars[9];
+  uint8_t* sK = sQ + FA_TILE;    // 2 stages
+  uint8_t* sV = sK + 2 * PF_KV;  // 2 stages
+  __shared__ __align__(8) uint64_t bars[15];
   uint64_t* q_full = bars + 0;
-  uint64_t* k_full = bars + 1;
-  uint64_t* k_empty = bars + 2;
-  uint64_t* v_full = bars + 3;
-  uint64_t* v_empty = bars + 4;
-  uint64_t* s_full = bars + 5;
-  uint64_t* p_full = bars + 6;  // one arrival per softmax warp
-  uint64_t* o_done = bars + 7;  // O += P V_j done
-  uint64_t* drain = bars + 8;
+  uint64_t* k_full = bars + 1;   // [2 stages]
+  uint64_t* k_empty = bars + 3;  // [2 stages]
+  uint64_t* v_full = bars + 5;   // [2 stages]
+  uint64_t* v_empty = bars + 7;  // [2 stages]
+  uint64_t* s_full = bars + 9;   // [2 score tiles]
+  uint64_t* p_full = bars + 11;  // [2 score tiles] one arrival per softmax warp
+  uint64_t* o_done = bars + 13;  // O += P V of a tile done
+  uint64_t* drain = bars + 14;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   __shared__ int s_lo;  // first visible row of the tile's first query
@@ -114,17 +116,19 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
-    mbar_init(k_full, 1);
-    mbar_init(k_empty, 1);
-    mbar_init(v_full, 1);
-    mbar_init(v_empty, 1);
-    mbar_init(s_full, 1);
-    mbar_init(p_full, 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+    }
     mbar_init(o_done, 1);
     mbar_init(drain, 1);
     s_abort = 0;
     fence_mbar_init();
-    // Q and, under a causal mask always, the last key tile's K need no lookup
+    // (Q needs no lookup)
     mbar_arrive_expect_tx(q_full, FA_TILE);
     tma_load_2d(sQ, &tm_q, q_full, h * 128, q0);
     tma_load_2d(sQ + 16384, &tm_q, q_full, h * 128 + 64, q0);
@@ -145,51 +149,58 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int jlo = s_lo / FA_BN, jhi = min(q0 + FA_BM - 1, n_rows - 1) / FA_BN;
+  const int jlo = s_lo / PF_BN, jhi = min(q0 + FA_BM - 1, n_rows - 1) / PF_BN;
   const int n = jhi - jlo + 1;  // key tiles
 
   if (warp == 0) {
     if (lane == 0) {
       for (int i = 0; i < n; ++i) {
-        const uint32_t par = (i & 1) ^ 1u;
-        const int kr = (jlo + i) * FA_BN;
-        if (!mbar_wait(k_empty, par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(k_full, FA_TILE);
-        tma_load_2d(sK, &tm_k, k_full, kvh * 128, kr);
-        tma_load_2d(sK + 16384, &tm_k, k_full, kvh * 128 + 64, kr);
-        if (!mbar_wait(v_empty, par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
-        mbar_arrive_expect_tx(v_full, FA_TILE);
-        tma_load_2d(sV, &tm_v, v_full, kvh * 128, kr);
-        tma_load_2d(sV + 16384, &tm_v, v_full, kvh * 128 + 64, kr);
+        const int st = i & 1, kr = (jlo + i) * PF_BN;
+        const uint32_t par = ((i >> 1) & 1) ^ 1u;
+        uint8_t *k = sK + st * PF_KV, *v = sV + st * PF_KV;
+        if (!mbar_wait(&k_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&k_full[st], PF_KV);
+        tma_load_2d(k, &tm_k, &k_full[st], kvh * 128, kr);
+        tma_load_2d(k + 8192, &tm_k, &k_full[st], kvh * 128 + 64, kr);
+        if (!mbar_wait(&v_empty[st], par, abort_flag, ERRW_TIMEOUT_PRODUCER)) break;
+        mbar_arrive_expect_tx(&v_full[st], PF_KV);
+        tma_load_2d(v, &tm_v, &v_full[st], kvh * 128, kr);
+        tma_load_2d(v + 8192, &tm_v, &v_full[st], kvh * 128 + 64, kr);
       }
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t IDESC_S = make_idesc(128, 128, false, false, false);
+      constexpr uint32_t IDESC_S = make_idesc(128, PF_BN, false, false, false);
       constexpr uint32_t IDESC_O = make_idesc(128, 128, false, true, false);
-      const uint32_t aQ = smem_u32(sQ), aK = smem_u32(sK), aV = smem_u32(sV);
+      const uint32_t aQ = smem_u32(sQ);
       bool ok = mbar_wait(q_full, 0, abort_flag, ERRW_TIMEOUT_MMA);
       for (int i = 0; ok && i <= n; ++i) {
-        if (i > 0) {  // O += P V of the tile before, P read from TMEM
-          if (!mbar_wait(v_full, (i - 1) & 1, abort_flag, ERRW_TIMEOUT_MMA) ||
-              !mbar_wait(p_full, (i - 1) & 1, abort_flag, ERRW_TIMEOUT_MMA))
-            break;
+        if (i < n) {  // S of tile i
+          const int st = i & 1;
+          const uint32_t aK = smem_u32(sK + st * PF_KV);
+          if (!mbar_wait(&k_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) break;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            mma_bf16_ts(tmem + 128, tmem + k * 8, fa_desc_mn(aV, k), IDESC_O, (i > 1 || k > 0) ? 1u : 0u);
-          mma_commit(v_empty);
+            mma_bf16_ss(tmem + st * PF_BN, fa_desc_k(aQ, k),
+                        smem_desc_sw128(aK + (uint32_t)((k >> 2) * 8192 + (k & 3) * 32), 16, 1024), IDESC_S, k > 0 ? 1u : 0u);
+          mma_commit(&s_full[st]);
+          mma_commit(&k_empty[st]);
+        }
+        if (i > 0) {  // O += P V of tile i - 1, P read from TMEM
+          const int st = (i - 1) & 1;
+          const uint32_t par = ((i - 1) >> 1) & 1, aV = smem_u32(sV + st * PF_KV);
+          if (!mbar_wait(&v_full[st], par, abort_flag, ERRW_TIMEOUT_MMA) ||
+              !mbar_wait(&p_full[st], par, abort_flag, ERRW_TIMEOUT_MMA))
+            break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16_ts(tmem + 128, tmem + st * PF_BN + k * 8, smem_desc_sw128(aV + (uint32_t)(k * 2048), 8192, 1024),
+                        IDESC_O, (i > 1 || k > 0) ? 1u : 0u);
+          mma_commit(&v_empty[st]);
           mma_commit(o_done);
         }
-        if (i == n) break;
-        // S: products of one thread run in order, so it overwrites P after the
-        // product that reads it
-        if (!mbar_wait(k_full, i & 1, abort_flag, ERRW_TIMEOUT_MMA)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mma_bf16_ss(tmem, fa_desc_k(aQ, k), fa_desc_k(aK, k), IDESC_S, k > 0 ? 1u : 0u);
-        mma_commit(s_full);
-        mma_commit(k_empty);
       }
       if (*abort_flag) {
         mma_commit(drain);
@@ -206,20 +217,20 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
-      const int k0 = (jlo + c) * FA_BN;
-      ok = mbar_wait_warp(s_full, c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      const int k0 = (jlo + c) * PF_BN, st = c & 1;
+      const uint32_t s_addr = lane_addr + st * PF_BN;
+      ok = mbar_wait_warp(&s_full[st], (c >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
       if (!ok) break;
       tc_fence_after();
-      uint32_t v[128];
+      uint32_t v[64];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tmem_ld_32x32b_x32(lane_addr + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
+      for (int k = 0; k < 2; ++k) tmem_ld_32x32b_x32(s_addr + k * 32, *reinterpret_cast<uint32_t(*)[32]>(&v[k * 32]));
       tmem_ld_wait();
       // rows are masked in a tile that reaches past the first query, or
       // before what the last one sees (kv_lo grows with the row)
-      if (__any_sync(0xffffffffu, k0 < kv_lo || k0 + FA_BN - 1 > kv_hi)) {
+      if (__any_sync(0xffffffffu, k0 < kv_lo || k0 + PF_BN - 1 > kv_hi)) {
 #pragma unroll
-        for (int i = 0; i < 128; ++i) {
+        for (int i = 0; i < PF_BN; ++i) {
           const int jk = k0 + i;
           v[i] = (jk >= kv_lo && jk <= kv_hi) ? v[i] : __float_as_uint(-INFINITY);
         }
@@ -228,9 +239,13 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
 #pragma unroll
       for (int i = 0; i < 8; ++i) mp[i] = __uint_as_float(v[i]);
 #pragma unroll
-      for (int i = 8; i < 128; ++i) mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
-      const float mx =
-          fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])), fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7]))) * sl2;
+      for (int i = 8; i < 56; i += 16) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mp[k] = fmax3(mp[k], __uint_as_float(v[i + k]), __uint_as_float(v[i + 8 + k]));
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mp[k] = fmaxf(mp[k], __uint_as_float(v[56 + k]));
+      const float mx = fmax3(fmax3(mp[0], mp[1], mp[2]), fmax3(mp[3], mp[4], mp[5]), fmaxf(mp[6], mp[7])) * sl2;
       // the running max moves only when it grows by more than 8 (base 2)
       const bool grow = mx > m_used + 8.f;
       const float corr = grow ? fast_exp2(m_used - mx) : 1.f;  // 0 when m_used is -inf
@@ -239,35 +254,38 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
         m_used = mx;
       }
       const float mu = (m_used == -INFINITY) ? 0.f : m_used;
-      // P = exp2(s*scale - m) as bf16 pairs (key 2c in the low half) over the
-      // first 64 columns of S
-      float lp[4] = {0.f, 0.f, 0.f, 0.f};
+      // P = exp2(s*scale - m) as bf16 pairs (key 2c in the low half)
+      const f32x2 sl2_2 = f2_pack(sl2, sl2), mu_2 = f2_pack(-mu, -mu);
+      f32x2 lp[2] = {0, 0};
 #pragma unroll
-      for (int hq = 0; hq < 4; ++hq) {  // 32 keys (16 columns of P) at a time
+      for (int hq = 0; hq < 2; ++hq) {  // 32 keys (16 columns of P) at a time
         uint32_t pk[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           const int i = hq * 32 + 2 * e;
-          const float p0 = fast_exp2(fmaf(__uint_as_float(v[i]), sl2, -mu));  // exp2(-inf) = 0 for masked keys
-          const float p1 = fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl2, -mu));
-          lp[(2 * e) & 3] += p0;
-          lp[(2 * e + 1) & 3] += p1;
+          float p0, p1;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2_2, mu_2), p0, p1);
+          p0 = fast_exp2(p0);  // exp2(-inf) = 0 for masked keys
+          p1 = fast_exp2(p1);
+          lp[e & 1] = f2_add(lp[e & 1], f2_pack(p0, p1));
           pk[e] = pack_bf16(p0, p1);
         }
-        tmem_st_32x32b_x16(lane_addr + hq * 16, pk);
+        tmem_st_32x32b_x16(s_addr + hq * 16, pk);
       }
-      l += (lp[0] + lp[1]) + (lp[2] + lp[3]);
+      float l0, l1;
+      f2_unpack(f2_add(lp[0], lp[1]), l0, l1);
+      l += l0 + l1;
       // V rows behind the last sequence may hold anything (0 * NaN is NaN):
       // they are zeroed before the product that reads them
-      if (n_rows < total && k0 + FA_BN > n_rows) {
-        ok = mbar_wait_warp(v_full, c & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+      if (n_rows < total && k0 + PF_BN > n_rows) {
+        ok = mbar_wait_warp(&v_full[st], (c >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
-        if (k0 + r >= n_rows) zero_tile_row(sV, 16384, r);
+        if (r < PF_BN && k0 + r >= n_rows) zero_tile_row(sV + st * PF_KV, 8192, r);
         fence_proxy_async_smem();
       }
-      // O to the new max (the TMEM accesses are warp-collective: the whole
-      // warp enters, rows that keep their max use 1).  O holds every PV product
-      // up to tile c-1 (the commit of S above follows them); the wait states it.
+      // O to the new max, once it holds every PV product up to tile c-1 (the
+      // TMEM accesses are warp-collective: the whole warp enters, rows that keep
+      // their max use 1)
       if (c > 0 && __any_sync(0xffffffffu, grow)) {
         ok = mbar_wait_warp(o_done, (c - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
@@ -285,7 +303,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+      if (lane == 0) mbar_arrive(&p_full[st]);
     }
     if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(o_done, (n - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
       tc_fence_after();
