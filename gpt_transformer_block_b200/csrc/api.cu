@@ -209,35 +209,29 @@ int allow_smem(K kernel, int bytes, SmemOnce& once) {
 }
 SmemOnce g_smem_packed_fwd, g_smem_packed_bwd, g_smem_prefix;
 
+// A launch with clusters of cs CTAs (1: none); `dependent`: the kernel waits
+// with pdl_wait() and is set up while the one before it in the stream ends.
 template <class... P, class... A>
-cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cs, cudaStream_t st,
-                           A... args) {
+cudaError_t launch_ex(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, int cs, bool dependent,
+                      cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = (unsigned)cs;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  if (cs > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs].val.clusterDim.x = (unsigned)cs;
+    at[cfg.numAttrs].val.clusterDim.y = at[cfg.numAttrs].val.clusterDim.z = 1;
+    ++cfg.numAttrs;
+  }
+  if (dependent) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+    ++cfg.numAttrs;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
-}
-
-// a kernel that begins with pdl_wait(), set up while the one before it in the stream ends
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
@@ -1626,12 +1620,12 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
   // CTAs per chain of steps: as many as the SMs have room for at once
   int cs = 1;
   while (cs < PB_CLUSTER && grid * cs * 2 <= sms) cs *= 2;
-  CK(launch_cluster(packed_attn_bwd_kernel, (unsigned)(grid * cs), AB2_THREADS, AB2_SMEM, cs, st, tq, tk, tv, tdo, tdk, tdv,
+  CK(launch_ex(packed_attn_bwd_kernel, (unsigned)(grid * cs), AB2_THREADS, AB2_SMEM, cs, true, st, tq, tk, tv, tdo, tdk, tdv,
                     static_cast<bf16*>(dk), lddk, static_cast<bf16*>(dv), lddv, lse, D, acc, cu_seqlens, n_seq, total, H,
                     Hkv, window, cs));
   CKL();
-  packed_attn_dq_kernel<<<blocks((long long)total * H * 16), 256, 0, st>>>(acc, static_cast<bf16*>(dq), lddq, cu_seqlens,
-                                                                           n_seq, total, H);
+  CK(launch_ex(packed_attn_dq_kernel, (unsigned)blocks((long long)total * H * 16), 256, 0, 1, true, st, acc,
+               static_cast<bf16*>(dq), lddq, cu_seqlens, n_seq, total, H));
   CKL();
   return GPTB_OK;
 }
@@ -1729,7 +1723,7 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
   prefix_split_kernel<<<grid, PD_THREADS, PD_SMEM, st>>>(tqp, tqo, tkp, tvp, tko, tvo, a);
   CKL();
   // set up while the split kernel ends
-  CK(launch_dependent(prefix_combine_kernel, (unsigned)(B * H), 128, st, a, static_cast<bf16*>(o),
+  CK(launch_ex(prefix_combine_kernel, (unsigned)(B * H), 128, 0, 1, true, st, a, static_cast<bf16*>(o),
                       lse, grid));
   CKL();
   return GPTB_OK;
@@ -1758,7 +1752,7 @@ int policy_rows(const T* z, T* dz, PolicyArgs a, int* parts, cudaStream_t st) {
   const long long fill = std::min(ctas / a.rows, row / (2 * POL_THREADS));
   a.cs = (int)std::min<long long>(POL_CLUSTER, std::max(hold, fill));
   *parts = (int)std::max(1ll, std::min<long long>(a.rows, std::min<long long>(POL_MAX_PARTS, ctas / a.cs)));
-  CK(launch_cluster(policy_rows_kernel<T, ALIGNED>, (unsigned)(*parts * a.cs), POL_THREADS, POL_SMEM, a.cs, st, z, dz, a));
+  CK(launch_ex(policy_rows_kernel<T, ALIGNED>, (unsigned)(*parts * a.cs), POL_THREADS, POL_SMEM, a.cs, false, st, z, dz, a));
   CKL();
   return GPTB_OK;
 }
@@ -1813,7 +1807,7 @@ int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int 
   int parts = 0;
   TRY(dtype == GPTB_F32 ? policy_launch<float>(logits, dlogits, a, &parts, st)
                         : policy_launch<bf16>(logits, dlogits, a, &parts, st));
-  policy_stats_kernel<<<1, 96, 0, st>>>(a.part, parts, stats);
+  CK(launch_ex(policy_stats_kernel, 1, 96, 0, 1, true, st, a.part, parts, stats));
   CKL();
   return GPTB_OK;
 }

@@ -426,6 +426,21 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
     tma_prefetch_desc(&tm_do);
     tma_prefetch_desc(&tm_dk);
     tma_prefetch_desc(&tm_dv);
+    // K and V, and where the chain has one CTA the first step's Q and dO: they
+    // need no lookup
+    mbar_arrive_expect_tx(kv_full, 2 * AB2_KV_TILE);
+    tma_load_2d(sK, &tm_k, kv_full, kvh * 128, k0);
+    tma_load_2d(sK + 16384, &tm_k, kv_full, kvh * 128 + 64, k0);
+    tma_load_2d(sV, &tm_v, kv_full, kvh * 128, k0);
+    tma_load_2d(sV + 16384, &tm_v, kv_full, kvh * 128 + 64, k0);
+    if (cs == 1) {
+      const int hh = kvh * G, q0 = k0;
+      mbar_arrive_expect_tx(&qdo_full[0], 2 * AB2_Q_TILE);
+      tma_load_2d(sQ, &tm_q, &qdo_full[0], hh * 128, q0);
+      tma_load_2d(sQ + 8192, &tm_q, &qdo_full[0], hh * 128 + 64, q0);
+      tma_load_2d(sDO, &tm_do, &qdo_full[0], hh * 128, q0);
+      tma_load_2d(sDO + 8192, &tm_do, &qdo_full[0], hh * 128 + 64, q0);
+    }
   }
   // queries that see a softmax thread's key: [key, key + W] inside its sequence
   int q_vis_hi = -1;
@@ -443,6 +458,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_launch();
+  pdl_wait();  // (D, and the dQ sums set to 0)
   const int q_first = s_vis[0];
   const int qt_lo = k0 / AB2_BQ;
   const int nq = s_vis[1] / AB2_BQ - qt_lo + 1;
@@ -452,13 +469,6 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      mbar_arrive_expect_tx(kv_full, 2 * AB2_KV_TILE);
-      tma_load_2d(sK, &tm_k, kv_full, kvh * 128, k0);
-      tma_load_2d(sK + 16384, &tm_k, kv_full, kvh * 128 + 64, k0);
-      tma_load_2d(sV, &tm_v, kv_full, kvh * 128, k0);
-      tma_load_2d(sV + 16384, &tm_v, kv_full, kvh * 128 + 64, k0);
-    }
     bool ok = true;
     for (int i = 0; i < steps && ok; ++i) {
       const int st = i % AB2_STAGES;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
       if (!ok) break;
       // the tile loads go out first; LSE and D (plain loads, guarded at the
       // sequence end) overlap them and complete the stage with a second arrival
-      if (lane == 0) {
+      if (lane == 0 && (i > 0 || cs > 1)) {
         mbar_arrive_expect_tx(&qdo_full[st], 2 * AB2_Q_TILE);
         uint8_t* q = sQ + st * AB2_Q_TILE;
         uint8_t* d = sDO + st * AB2_Q_TILE;
@@ -797,6 +807,7 @@ __global__ void __launch_bounds__(256)
                            float* __restrict__ D, float* __restrict__ dq, const int32_t* __restrict__ cu, int n_seq,
                            int total, int H, int Hkv, int window, int rows, int few_ctas) {
   __shared__ int s_first[PB_PRE_ROWS];  // first visible row of each of the CTA's rows
+  pdl_launch();  // (the main kernel's CTAs take the place of those that end)
   const int n_rows = packed_rows(cu, n_seq, total);
   if (blockIdx.x == 0) packed_check(cu, n_seq, total);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -874,6 +885,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     packed_attn_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long lddq,
                           const int32_t* __restrict__ cu, int n_seq, int total, int H) {
+  pdl_wait();  // (the sums)
   const int n_rows = packed_rows(cu, n_seq, total);
   const int per_row = H * 16;
   const long long n = (long long)n_rows * per_row;

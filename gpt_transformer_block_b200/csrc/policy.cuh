@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   __shared__ double s_sum[3];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % a.cs, at = blockIdx.x / a.cs, n = gridDim.x / a.cs;
+  pdl_launch();  // (policy_stats_kernel may be set up; it waits for this grid to end)
   uint4* slot = pol_slots + tid;  // slot j of this thread: slot[j * POL_THREADS]
   int first, end;
   if (a.weights) {
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
 }
 
 // the clusters' sums, added in a fixed order: one warp per statistic
-__global__ void __launch_bounds__(96) policy_stats_kernel(const double* __restrict__ part, int n, float* __restrict__ stats) {
+__global__ void __launch_bounds__(96) policy_stats_kernel(const double* part, int n, float* __restrict__ stats) {
+  pdl_wait();  // (the sums)
   const int q = threadIdx.x >> 5, lane = threadIdx.x & 31;
   double v = 0.0;
   for (int i = lane; i < n; i += 32) v += part[i * 3 + q];
