@@ -10,8 +10,9 @@ from __future__ import annotations
 import torch
 
 from . import (BF16, F32, WS_BLOCK_SAVED, WS_BLOCK_SCRATCH, WS_LM_HEAD, WS_STACK, block_grads,
-               block_weights, gpt_block_backward, gpt_block_forward, gpt_stack_step, gptb_workspace_bytes,
-               lm_head_xent, make_config, model_grads, model_weights)
+               block_weights, gpt_block_backward, gpt_block_forward, gpt_stack_step, gptb_gemm_bf16, gptb_policy_loss,
+               gptb_policy_loss_workspace_bytes, gptb_token_logprobs, gptb_workspace_bytes, lm_head_xent, make_config,
+               model_grads, model_weights)
 
 
 def storage_torch_dtype(c: dict) -> torch.dtype:
@@ -113,4 +114,47 @@ def lm_head(c: dict, h, w_lm, targets, dh, dw_lm, stream=None):
     return loss
 
 
-__all__ = ["GPTStack", "BlockRunner", "to_device_weights", "zero_grads_like", "lm_head", "BF16", "F32"]
+def _logits(h, w_lm, out):
+    (n, d), V = h.shape, w_lm.shape[0]
+    gptb_gemm_bf16(h, 0, h.stride(0), w_lm, 0, d, out, 0, V, n, V, d)
+
+
+def lm_head_logprobs(h, w_lm, tokens, rows_per_chunk=8192):
+    """Log-probabilities [N] of the given tokens under logits h w_lm^T (bf16 h [N, d], w_lm [V, d]), a chunk of rows at
+    a time, on the current stream: what the sampling and the reference policy hand to lm_head_policy."""
+    N, V = h.shape[0], w_lm.shape[0]
+    logp = torch.empty(N, dtype=torch.float32, device=h.device)
+    z = torch.empty(min(N, rows_per_chunk), V, dtype=torch.bfloat16, device=h.device)
+    for i in range(0, N, rows_per_chunk):
+        n = min(rows_per_chunk, N - i)
+        _logits(h[i:i + n], w_lm, z[:n])
+        gptb_token_logprobs(z[:n], tokens[i:i + n], logp[i:i + n])
+    return logp
+
+
+def lm_head_policy(h, w_lm, actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, dh, dw_lm,
+                   rows_per_chunk=8192):
+    """The lm_head with the clipped policy loss in the place of the cross entropy: logits h w_lm^T of bf16 h [N, d] and
+    w_lm [V, d] (d and V multiples of 8), gptb_policy_loss over them, and the gradients dh (bf16 [N, d], overwritten)
+    and dw_lm (fp32 [V, d], accumulated).  A chunk of rows at a time, the gradient over the logits, so the [N, V]
+    logits never exist whole; on the current stream.  Returns (stats [3]: loss, KL, clipped weight; logp [N])."""
+    (N, d), V = h.shape, w_lm.shape[0]
+    stats = torch.zeros(3, dtype=torch.float32, device=h.device)
+    logp = torch.empty(N, dtype=torch.float32, device=h.device)
+    part = torch.empty(3, dtype=torch.float32, device=h.device)
+    rows = max(1, min(N, rows_per_chunk))
+    z = torch.empty(rows, V, dtype=torch.bfloat16, device=h.device)
+    ws = _ws(gptb_policy_loss_workspace_bytes(rows), h.device)
+    for i in range(0, N, rows_per_chunk):
+        n, at = min(rows_per_chunk, N - i), slice(i, min(N, i + rows_per_chunk))
+        _logits(h[at], w_lm, z[:n])
+        gptb_policy_loss(z[:n], actions[at], weights[at], advantages[at], logp_old[at],
+                         None if logp_ref is None else logp_ref[at], clip_lo, clip_hi, beta, z[:n], logp[at], part, ws)
+        gptb_gemm_bf16(z, 0, V, w_lm, 1, d, dh[at], 0, dh.stride(0), n, d, V)
+        gptb_gemm_bf16(z, 1, V, h[at], 1, h.stride(0), dw_lm, 1, d, V, d, n)
+        stats += part
+    return stats, logp
+
+
+__all__ = ["GPTStack", "BlockRunner", "to_device_weights", "zero_grads_like", "lm_head", "lm_head_logprobs",
+           "lm_head_policy", "BF16", "F32"]
