@@ -62,17 +62,17 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
 // warps: 0 TMA producer (Q once; K and V tiles of 64 keys, two stages each), 1
 // TMEM owner and MMA issuer, 2-5 softmax (thread = query row, its TMEM lane).
 // S = Q K^T of tile i in TMEM columns 64 (i % 2) .., P (bf16 pairs) over the
-// first half of it, O in columns 128-255.  The products of one thread run in
-// order, S of tile i+1 is issued before PV of tile i, so the softmax warps find
-// the next scores ready and the tensor core works while they do; the next S but
-// one overwrites P after the product that reads it.  O is rescaled only when a
+// first half of it, O in columns 128-255.  S of tile i+1 is issued before PV of
+// tile i, so the softmax warps find the next scores ready and the tensor core
+// works while they do.  O is rescaled only when a
 // row's running maximum grows by more than 8 in base 2 (P stays below 256 in
 // bf16, and the normalisation uses the same maximum, so the result is exact).
 // What bounds it: the softmax (its exponentials alone take half of the time on
 // their unit), and the start and end of a CTA, which the other CTA of the SM
-// fills.  One sequence of 8192 rows, 12 heads: FWD_NOTE us; with 128-key tiles
-// and so no room for a second S 204, as one CTA of two query tiles per SM
-// (attention_tc.cuh) 220.
+// fills.  One sequence of 8192 rows, 12 heads: 205 us, 24 ragged
+// ones (1 to 2000 rows, 10 heads, window 1024): 65 us; with 128-key tiles and so
+// no room for a second S 204 and 73, as one CTA of two query tiles per SM
+// (attention_tc.cuh) 220 and 84.
 constexpr int PF_THREADS = 192;
 constexpr int PF_BN = 64;
 constexpr int PF_KV = PF_BN * 128 * 2;                     // one K or V tile: two 64-column swizzled halves of 8 KB
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   uint8_t* sQ = smem;
   uint8_t* sK = sQ + FA_TILE;    // 2 stages
   uint8_t* sV = sK + 2 * PF_KV;  // 2 stages
-  __shared__ __align__(8) uint64_t bars[15];
+  __shared__ __align__(8) uint64_t bars[16];
   uint64_t* q_full = bars + 0;
   uint64_t* k_full = bars + 1;   // [2 stages]
   uint64_t* k_empty = bars + 3;  // [2 stages]
@@ -96,8 +96,9 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   uint64_t* v_empty = bars + 7;  // [2 stages]
   uint64_t* s_full = bars + 9;   // [2 score tiles]
   uint64_t* p_full = bars + 11;  // [2 score tiles] one arrival per softmax warp
-  uint64_t* o_done = bars + 13;  // O += P V of a tile done
-  uint64_t* drain = bars + 14;
+  uint64_t* o_done = bars + 13;  // [2 score tiles] O += P V done (one barrier for all would be a phase behind or
+                                 // two: PV of the tile before may still run when a softmax ends)
+  uint64_t* drain = bars + 15;
   __shared__ uint32_t tmem_slot;
   __shared__ int s_abort;
   __shared__ int s_lo;  // first visible row of the tile's first query
@@ -123,8 +124,8 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
     }
-    mbar_init(o_done, 1);
     mbar_init(drain, 1);
     s_abort = 0;
     fence_mbar_init();
@@ -179,6 +180,9 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
           const int st = i & 1;
           const uint32_t aK = smem_u32(sK + st * PF_KV);
           if (!mbar_wait(&k_full[st], (i >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) break;
+          // it overwrites P of tile i - 2: products of different shapes may
+          // overlap, so the one that reads it has to be done
+          if (i >= 2 && !mbar_wait(&o_done[st], ((i >> 1) - 1) & 1, abort_flag, ERRW_TIMEOUT_MMA)) break;
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -199,7 +203,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
             mma_bf16_ts(tmem + 128, tmem + st * PF_BN + k * 8, smem_desc_sw128(aV + (uint32_t)(k * 2048), 8192, 1024),
                         IDESC_O, (i > 1 || k > 0) ? 1u : 0u);
           mma_commit(&v_empty[st]);
-          mma_commit(o_done);
+          mma_commit(&o_done[st]);
         }
       }
       if (*abort_flag) {
@@ -287,7 +291,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       // TMEM accesses are warp-collective: the whole warp enters, rows that keep
       // their max use 1)
       if (c > 0 && __any_sync(0xffffffffu, grow)) {
-        ok = mbar_wait_warp(o_done, (c - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+        ok = mbar_wait_warp(&o_done[st ^ 1], ((c - 1) >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
         tc_fence_after();
 #pragma unroll 1
@@ -305,7 +309,8 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_full[st]);
     }
-    if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(o_done, (n - 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE)) {
+    if (__all_sync(0xffffffffu, ok) && mbar_wait_warp(&o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag,
+                                                       ERRW_TIMEOUT_EPILOGUE)) {
       tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       // O (bf16) leaves through the Q tile, free once every S product has
@@ -361,7 +366,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
 // where there are fewer chains than SMs a cluster of up to 8 CTAs shares each:
 // every CTA takes a part of its steps, and the partial dK and dV meet through
 // distributed shared memory, added in a fixed order (5 sequences of 12 to 180
-// tokens, 8 query heads over 2: CLUSTER_NOTE).
+// tokens, 8 query heads over 2: 47 us with one CTA per chain, 30 with 8).
 constexpr int PB_CLUSTER = 8;
 __global__ void __launch_bounds__(AB2_THREADS, 1)
     packed_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -782,7 +787,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
 // 1 / sqrt(visible keys).  So for rows that see at most PB_FEW keys D is taken
 // as the sum of P dP, which needs no o: two lanes per key, by CTAs of their own.  (Without it dq and
 // dk of 5 sequences of 12 to 180 tokens were 2.6e-3 off in the norm, with it
-// FEW_NOTE; 1.7e-3 is the rounding of the result alone.)
+// 2.4e-3; 1.7e-3 is the rounding of the result alone.)
 constexpr int PB_FEW = 16;
 constexpr int PB_PRE_ROWS = 16;  // most rows of a CTA
 

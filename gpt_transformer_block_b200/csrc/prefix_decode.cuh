@@ -401,6 +401,10 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         ok = mbar_wait(&k_full[st], (n / PD_ST) & 1, abort_flag, ERRW_TIMEOUT_MMA);
         if (!ok) return 0;
         const volatile PdTile& d = ring[n % PD_RING];
+        // S overwrites P of tile n - 2: products of different shapes may
+        // overlap, so the one that reads it has to be done
+        if (n >= 2) ok = mbar_wait(&o_done[t], ((n - 2) >> 1) & 1, abort_flag, ERRW_TIMEOUT_MMA);
+        if (!ok) return 0;
         const int fl = d.flags;
         if (fl & PD_END) {
           end = true;

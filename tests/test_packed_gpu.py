@@ -137,6 +137,20 @@ def test_packed_rows_do_not_depend_on_their_neighbours(cuda_lib):
         assert torch.equal(a, b)
 
 
+def test_packed_forward_same_bits_every_time(cuda_lib):
+    """Two CTAs on every multiprocessor and long rows: a product that overtook the one before it would show."""
+    gb = cuda_lib
+    for lens, H, Hk, window, times in (([6000, 37, 1500], 12, 12, -1, 40), ([300, 900, 45] * 8, 10, 5, 700, 60)):
+        qkv, _, cu = packed(lens, H, Hk, seed=11)
+        q, k, v = qkv_views(qkv, H, Hk)
+        outs = [torch.empty(len(q), H * 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        lse = torch.empty(H, len(q), device="cuda")
+        gb.gptb_packed_attention(q, k, v, cu, outs[0], lse, H, Hk, window)
+        for _ in range(times):
+            gb.gptb_packed_attention(q, k, v, cu, outs[1], lse, H, Hk, window)
+            assert torch.equal(*outs)
+
+
 def test_packed_captured_call_follows_its_lengths(cuda_lib):
     """A captured forward and backward, replayed with other lengths in the same offsets array, on a stream of its own."""
     gb = cuda_lib

@@ -102,7 +102,7 @@ def test_prefix_decode_large_batch_same_bits_every_time(cuda_lib):
     lens = g.integers(1, 400, 90).tolist()
     d = prefix_case([900, 2000, 40], [30, 50, 10], lens, 400, 4, 2, seed=6)
     first = check(gb, d, 4, 2, -1)
-    for _ in range(3):
+    for _ in range(100):
         assert torch.equal(call(gb, d, 4, 2, -1)[0], first)
 
 
