@@ -111,8 +111,8 @@ def prefix_decode(q, k_prefix, v_prefix, cu_prefix, cu_group, k_cache, v_cache, 
 
 def token_logprobs(z, tokens):
     z = np.asarray(z, dtype=np.float64)
-    _, lse = _softmax(z)
-    return z[np.arange(len(z)), tokens] - lse
+    z = z - z.max(-1, keepdims=True)  # (first: z - lse loses lse where a whole row is the type's lowest value)
+    return z[np.arange(len(z)), tokens] - np.log(np.exp(z).sum(-1))
 
 
 def policy_loss(z, actions, weights, adv, lp_old, lp_ref, clip_lo, clip_hi, beta):
@@ -127,8 +127,8 @@ def policy_loss(z, actions, weights, adv, lp_old, lp_ref, clip_lo, clip_hi, beta
         w, A = float(weights[i]), float(adv[i])
         if w == 0.0 or not 0 <= actions[i] < V:
             continue
-        p, lse = _softmax(z[i][None])
-        lp = z[i, actions[i]] - lse[0]
+        p, _ = _softmax(z[i][None])
+        lp = token_logprobs(z[i][None], [actions[i]])[0]
         r = np.exp(lp - float(lp_old[i]))
         lo, hi = 1.0 - clip_lo, 1.0 + clip_hi
         un, cl = r * A, min(max(r, lo), hi) * A

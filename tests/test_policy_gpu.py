@@ -184,3 +184,25 @@ def test_policy_no_rows(cuda_lib):
     _, _, stats = call(gb, {n: t[:0] for n, t in d.items()})
     assert torch.all(stats == 0)
     gb.gptb_token_logprobs(d["z"][:0], d["a"][:0], torch.empty(0, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [600, 40001])
+def test_logits_of_the_types_lowest_and_large_ones(cuda_lib, dtype, V):
+    """Rows masked with the type's lowest value, in part and whole (a uniform softmax), and logits around 1e4."""
+    gb = cuda_lib
+    d = policy_case(5, V, dtype, seed=12, masked=0.0)
+    low = torch.finfo(dtype).min
+    a = d["a"].long()
+    d["z"][0] = low
+    keep = d["z"][1].clone()
+    d["z"][1, : V // 2] = low
+    d["z"][1, a[1]] = keep[a[1]]
+    d["z"][2] = low
+    d["z"][2, a[2]] = 1.0
+    d["z"][3] += 1e4
+    d["z"][4] = float("-inf")
+    d["z"][4, a[4]] = low
+    lp = torch.log_softmax(d["z"].double(), -1)[torch.arange(5), a]
+    d["old"], d["ref"] = (lp + 0.05).float(), (lp - 0.1).float()
+    check(gb, d)

@@ -162,3 +162,50 @@ def test_an_operator_on_a_stream_of_its_own(cuda_lib):
     gb.gptb_packed_attention(late[:, :256], late[:, 256:384], late[:, 384:], cu, o, lse, 2, 1, stream=s)
     s.synchronize()
     assert torch.equal(o, want)
+
+
+def test_two_calls_at_once(cuda_lib):
+    """Calls of each operator on two streams at the same time, with outputs and workspaces of their own."""
+    gb = cuda_lib
+    g = torch.Generator().manual_seed(7)
+    n, V = 900, 4001
+    x = normed(g, n, H + 2 * HK, 128).view(n, W).cuda()
+    dout = torch.randn(n, H * 128, generator=g).bfloat16().cuda()
+    cu = torch.tensor([0, 300, 310, 900], dtype=torch.int32, device="cuda")
+    cg = torch.tensor([0, 2, 5, 6], dtype=torch.int32, device="cuda")
+    kc, vc = (normed(g, 6, 40, HK, 128).cuda() for _ in range(2))
+    lens = torch.tensor([1, 40, 7, 0, 33, 12], dtype=torch.int32, device="cuda")
+    z = torch.randn(n, V, generator=g).cuda()
+    a = torch.randint(0, V, (n,), generator=g, dtype=torch.int32).cuda()
+    row = [torch.randn(n, generator=g).cuda() for _ in range(4)]
+    q, k, v = x[:, :H * 128], x[:, H * 128:(H + HK) * 128], x[:, (H + HK) * 128:]
+
+    def buffers():
+        e = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+        bf, u8 = torch.bfloat16, torch.uint8
+        return {"o": e(n, H * 128, dt=bf), "lse": e(H, n), "dk": e(n, HK * 128, dt=bf), "dv": e(n, HK * 128, dt=bf),
+                "dq": e(n, H * 128, dt=bf), "ws": e(gb.gptb_packed_attention_workspace_bytes(n, H), dt=u8),
+                "od": e(6, H, 128, dt=bf), "ld": e(6, H), "wd": e(gb.gptb_prefix_decode_workspace_bytes(6, H, HK), dt=u8),
+                "dz": e(n, V), "logp": e(n), "stats": e(3), "wp": e(gb.gptb_policy_loss_workspace_bytes(n), dt=u8)}
+
+    def enqueue(b, s):
+        gb.gptb_packed_attention(q, k, v, cu, b["o"], b["lse"], H, HK, -1, s)
+        gb.gptb_packed_attention_backward(q, k, v, b["o"], dout, b["lse"], cu, b["dq"], b["dk"], b["dv"], H, HK, -1, b["ws"], s)
+        gb.gptb_prefix_decode_attention(b["o"][:6], k, v, cu, cg, kc, vc, lens, b["od"], b["ld"], H, HK, -1, b["wd"], s)
+        gb.gptb_policy_loss(z, a, row[0], row[1], row[2], row[3], 0.2, 0.2, 0.1, b["dz"], b["logp"], b["stats"], b["wp"], s)
+
+    want = buffers()
+    enqueue(want, None)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [buffers() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for b, s in zip(got, streams):
+            enqueue(b, s)
+    torch.cuda.synchronize()
+    for b in got:
+        for name in ("o", "lse", "dk", "dv", "od", "ld", "dz", "logp", "stats"):
+            assert torch.equal(b[name], want[name]), name
+        # dq: fp32 sums in another order may round to the neighbouring bf16
+        assert (b["dq"].float() - want["dq"].float()).abs().max() <= 2.0 ** -7 * want["dq"].float().abs().max()
+    assert gb.gptb_device_error() == 0
