@@ -13,20 +13,20 @@
 //
 // Bound by HBM: one read of the rows that count and one write of the gradient.
 // A row is held in shared memory between the three steps that need it (maximum,
-// sum of exponentials, gradient), 66 KB of it by a CTA; what is longer comes back
-// from L2 for the gradient.  A few rows, or long ones, are shared out over the
-// CTAs of a cluster.  The next
-// row's loads go out as the gradient leaves, so that HBM stays busy through the
-// reductions (three CTAs per SM, 8192 bf16 rows of 32768 of which a third do not
-// count: 176 us, 5.1 TB/s; the exponentials, two per element, take about 0.6 of
-// the time on their unit, which the loads have to overlap with).  The row's few scalars, loaded a row ahead, are worked out in
-// double by one warp (the ratio is held against the clip borders, and the
-// exponentials of differences lose digits in fp32).
-// Rows that start on 16-byte boundaries are filled by asynchronous copies.  In
-// other ones vectors of 16 bytes are cut at the gradient's alignment, and where
-// the logits row starts elsewhere each is put together from two neighbouring
-// 16-byte loads (the second is the next lane's first: an L1 hit), so an odd
-// vocabulary streams like an even one.
+// sum of exponentials, gradient), 66 KB of it by a CTA; what is longer comes
+// back from L2 for the gradient.  A few rows, or long ones, are shared out over
+// the CTAs of a cluster.  The next row's asynchronous copies go out as the
+// gradient leaves, so that HBM stays busy through the reductions (three CTAs
+// per SM, 8192 bf16 rows of 32768 of which a third do not count: 177 us, 5.1
+// TB/s; the exponentials, two per element, take about 0.55 of the time on their
+// unit, which the loads have to overlap with).  The row's few scalars, loaded a
+// row ahead, are worked out in double by one warp (the ratio is held against
+// the clip borders, and the exponentials of differences lose digits in fp32).
+// Vectors of 16 bytes are cut at the logits' alignment, row by row; where the
+// gradient's row lies otherwise, each 16-byte store is put together from a
+// lane's vector and the next lane's, so an odd vocabulary streams like an even
+// one (2000 fp32 rows of 50257, gradient rows without padding: ODD_NOTE us;
+// with loads put together from two neighbours instead, through registers, 236).
 #pragma once
 #include <cfloat>
 
@@ -39,7 +39,6 @@ constexpr int POL_WARPS = POL_THREADS / 32;
 constexpr int POL_CTAS = 3;    // per SM
 constexpr int POL_KEEP = 11;   // 16-byte vectors of a row that a thread keeps
 constexpr int POL_SMEM = POL_KEEP * POL_THREADS * 16;  // 66 KB
-constexpr int POL_BATCH = 4;   // vectors that a thread has in flight where they pass through registers
 constexpr int POL_CLUSTER = 8; // most CTAs that share a row
 
 struct PolicyArgs {
@@ -87,62 +86,88 @@ struct PolVec<float> {
 };
 
 // A row of V elements as vectors of 16 bytes: vector i holds the elements
-// i N - p .. i N - p + N - 1 (p: how far the gradient's row lies past a 16-byte
+// i N - p .. i N - p + N - 1 (p: how far the logits' row lies past a 16-byte
 // boundary), the first and the last possibly in part.  ALIGNED: every row of
-// both arrays starts on a boundary (p = 0, and the logits are cut likewise).
+// both arrays starts on a boundary.
 template <class T, bool ALIGNED>
 struct PolicyRowView {
   static constexpr int N = PolVec<T>::N;
   const T* z;
   T* dz;
   int V, p, count;
-  int last;   // the first vector that reaches past the end
-  int shift;  // bytes from the 16-byte boundary below a vector's logits to them
-  __device__ __forceinline__ PolicyRowView(const T* z_, T* dz_, int V_) : z(z_), dz(dz_), V(V_), p(0), shift(0) {
-    if constexpr (!ALIGNED) {
-      const uintptr_t at = reinterpret_cast<uintptr_t>(dz ? (const T*)dz : z) & 15u;
-      p = (int)(at / sizeof(T));
-      shift = (int)((reinterpret_cast<uintptr_t>(z) - at) & 15u);
-    }
+  int last;  // the first vector that reaches past the end
+  int r;     // the gradient's next 16-byte boundary after a vector's first element, in elements (0: they lie alike)
+  __device__ __forceinline__ PolicyRowView(const T* z_, T* dz_, int V_) : z(z_), dz(dz_), V(V_) {
+    p = ALIGNED ? 0 : (int)((reinterpret_cast<uintptr_t>(z) & 15u) / sizeof(T));
     count = (V + p + N - 1) / N;
     last = (V + p) / N;
+    r = !ALIGNED && dz ? (p - (int)((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T)) + N) % N : 0;
   }
   __device__ __forceinline__ bool whole(int i) const { return (ALIGNED || i * N >= p) && i < last; }
   // vector i; elements outside the row are -inf
   __device__ __forceinline__ uint4 load(int i) const {
     const int e = i * N - p;
-    if (whole(i)) {
-      if (ALIGNED || shift == 0) return *reinterpret_cast<const uint4*>(z + e);
-      // (16 bytes from z + e on: both aligned words hold some of them)
-      if (e + N + N <= V && e >= N) {
-        const uint8_t* a = reinterpret_cast<const uint8_t*>(z + e) - shift;
-        const uint4 x = *reinterpret_cast<const uint4*>(a), y = *reinterpret_cast<const uint4*>(a + 16);
-        const bool two = shift & 8, one = shift & 4;
-        const uint32_t a0 = two ? x.z : x.x, a1 = two ? x.w : x.y, a2 = two ? y.x : x.z, a3 = two ? y.y : x.w,
-                       a4 = two ? y.z : y.x, a5 = two ? y.w : y.y;
-        const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? a4 : a3, b4 = one ? a5 : a4;
-        if constexpr (sizeof(T) == 4) return make_uint4(b0, b1, b2, b3);
-        const int h = (shift & 2) * 8;
-        return make_uint4(__funnelshift_r(b0, b1, h), __funnelshift_r(b1, b2, h), __funnelshift_r(b2, b3, h),
-                          __funnelshift_r(b3, b4, h));
-      }
-    }
+    if (whole(i)) return *reinterpret_cast<const uint4*>(z + e);
     float v[N];
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] = e + k >= 0 && e + k < V ? to_f(z[e + k]) : -INFINITY;
     return PolVec<T>::pack(v);
   }
-  __device__ __forceinline__ void store(int i, const uint4& u) const {
-    const int e = i * N - p;
-    if (whole(i)) {
-      *reinterpret_cast<uint4*>(dz + e) = u;
+  // The warp's vectors i (lane by lane, one after the other; those of lanes
+  // that are `in`) of the gradient.  A lane whose vector and the next lane's
+  // are whole stores the 16 bytes from its boundary on, the elements that no
+  // such store covers go out one by one.
+  __device__ __forceinline__ void store(int i, bool in, const uint4& u) const {
+    const int e = i * N - p, lane = threadIdx.x & 31;
+    const bool all = in && whole(i);
+    bool to = all, from = all;  // elements r .. N-1, and 0 .. r-1, are in a 16-byte store
+    if (ALIGNED || r == 0) {
+      if (all) *reinterpret_cast<uint4*>(dz + e) = u;
     } else {
+      uint4 y;
+      y.x = __shfl_down_sync(0xffffffffu, u.x, 1);
+      y.y = __shfl_down_sync(0xffffffffu, u.y, 1);
+      y.z = __shfl_down_sync(0xffffffffu, u.z, 1);
+      y.w = __shfl_down_sync(0xffffffffu, u.w, 1);
+      const unsigned wholes = __ballot_sync(0xffffffffu, all);
+      to = all && lane < 31 && (wholes >> ((lane + 1) & 31) & 1u);
+      from = all && lane > 0 && (wholes >> ((lane - 1) & 31) & 1u);
+      if (to) {
+        const int sh = r * (int)sizeof(T);
+        const bool two = sh & 8, one = sh & 4;
+        const uint32_t a0 = two ? u.z : u.x, a1 = two ? u.w : u.y, a2 = two ? y.x : u.z, a3 = two ? y.y : u.w,
+                       a4 = two ? y.z : y.x, a5 = two ? y.w : y.y;
+        const uint32_t b0 = one ? a1 : a0, b1 = one ? a2 : a1, b2 = one ? a3 : a2, b3 = one ? a4 : a3, b4 = one ? a5 : a4;
+        const int h = (sh & 2) * 8;
+        *reinterpret_cast<uint4*>(dz + e + r) =
+            sizeof(T) == 4 ? make_uint4(b0, b1, b2, b3)
+                           : make_uint4(__funnelshift_r(b0, b1, h), __funnelshift_r(b1, b2, h),
+                                        __funnelshift_r(b2, b3, h), __funnelshift_r(b3, b4, h));
+      }
+    }
+    if (in && !(to && from)) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        if (e + k >= 0 && e + k < V) dz[e + k] = from_f<T>(PolVec<T>::get(u, k));
+        if (!(ALIGNED || k >= r ? to : from) && e + k >= 0 && e + k < V) dz[e + k] = from_f<T>(PolVec<T>::get(u, k));
     }
   }
 };
+
+// part `rank` of n of a row of V zeros, by the CTA
+template <class T>
+__device__ __forceinline__ void policy_zero(T* dz, int V, int rank, int n) {
+  constexpr int N = PolVec<T>::N;
+  const int p = (int)((reinterpret_cast<uintptr_t>(dz) & 15u) / sizeof(T)), count = (V + p + N - 1) / N;
+  const int end = (int)((long long)count * (rank + 1) / n);
+  for (int i = (int)((long long)count * rank / n) + threadIdx.x; i < end; i += blockDim.x) {
+    const int e = i * N - p;
+    if (e >= 0 && e + N <= V) {
+      *reinterpret_cast<uint4*>(dz + e) = make_uint4(0, 0, 0, 0);
+    } else {
+      for (int k = max(0, e); k < min(V, e + N); ++k) dz[k] = from_f<T>(0.f);
+    }
+  }
+}
 
 // A row's scalars, copied to shared memory a row ahead (by one thread, which
 // waits for them before a barrier that the others wait at too).
@@ -255,7 +280,9 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   using Row = PolicyRowView<T, ALIGNED>;
   extern __shared__ __align__(16) uint4 pol_slots[];  // [POL_KEEP][POL_THREADS]
   __shared__ float sm[POL_WARPS], ss[POL_WARPS];
-  __shared__ float2 s_part[2];  // this CTA's maximum and sum of the row, by parity of the row
+  // This CTA's maximum and sum of the row, in turn: a CTA may be a row ahead of
+  // those that still read its part of the last one, not two.
+  __shared__ float2 s_part[2];
   __shared__ float s_g, s_inv;
   __shared__ int s_scan[POL_WARPS], s_range[2];
   __shared__ PolicyIn s_in[2];  // of rows i and i + 1, by parity
@@ -279,11 +306,11 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   // this CTA's vectors of a row are lo(row) .. hi(row) - 1; thread t has lo + t, lo + t + POL_THREADS, ...
   const auto lo = [&](const Row& r) { return (int)((long long)r.count * rank / a.cs); };
   const auto hi = [&](const Row& r) { return (int)((long long)r.count * (rank + 1) / a.cs); };
-  // one asynchronous copy (ALIGNED)
+  // one vector of a row into slot j
   const auto copy = [&](int j, const Row& r, int c) {
     if (r.whole(c))
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot + j * POL_THREADS)),
-                   "l"(r.z + (long long)c * N) : "memory");
+                   "l"(r.z + (c * N - r.p)) : "memory");
     else
       slot[j * POL_THREADS] = r.load(c);
   };
@@ -294,6 +321,7 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   }
   __syncthreads();
   bool have = false;  // the row is being loaded already
+  int turn = 0;       // of the rows that are read
   for (int i = first; i < end; ++i) {
     const Row row = view(i);
     const int c_lo = lo(row) + tid, c_hi = hi(row);
@@ -302,8 +330,7 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     if (tid == 0 && i + 1 < end) policy_in(a, i + 1, &s_in[(i + 1) & 1]);
     // (an action outside the vocabulary is reported, never read)
     if (w == 0.f || y < 0 || y >= a.V) {
-      if (dlogits)
-        for (int c = c_lo; c < c_hi; c += POL_THREADS) row.store(c, make_uint4(0, 0, 0, 0));
+      if (dlogits) policy_zero(row.dz, a.V, rank, a.cs);
       if (tid == 0) {
         if (rank == 0) {
           if (w != 0.f) record_error(ERRW_BAD_TARGET);
@@ -317,20 +344,9 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     const int kept = max(0, min(POL_KEEP, (c_hi - c_lo + POL_THREADS - 1) / POL_THREADS));
     const int c_rest = c_lo + POL_KEEP * POL_THREADS;  // the first vector that is not kept
     if (!have) {
-      if constexpr (ALIGNED) {
-        for (int j = 0; j < kept; ++j) copy(j, row, c_lo + j * POL_THREADS);
-      } else {
-        for (int j0 = 0; j0 < kept; j0 += POL_BATCH) {
-          uint4 u[POL_BATCH];
-#pragma unroll
-          for (int q = 0; q < POL_BATCH; ++q)
-            if (j0 + q < kept) u[q] = row.load(c_lo + (j0 + q) * POL_THREADS);
-#pragma unroll
-          for (int q = 0; q < POL_BATCH; ++q)
-            if (j0 + q < kept) slot[(j0 + q) * POL_THREADS] = u[q];
-        }
-      }
+      for (int j = 0; j < kept; ++j) copy(j, row, c_lo + j * POL_THREADS);
     }
+    turn ^= 1;
     const float za = to_f(row.z[y]);
     // this thread's maximum and sum of exponentials, then the row's
     float m = -FLT_MAX;  // (so that a strip of -inf adds 0)
@@ -371,12 +387,12 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     float S = 0.f;  // (warp 0)
     if (warp == 0) S = warp_sum(lane < POL_WARPS ? ss[lane] * fast_exp2((m_lane - m) * LOG2E) : 0.f);
     if (a.cs > 1) {  // the cluster's: each CTA reads the others' parts
-      if (tid == 0) s_part[i & 1] = make_float2(m, S);
+      if (tid == 0) s_part[turn] = make_float2(m, S);
       cluster_sync_all();
       float2 part = make_float2(-FLT_MAX, 0.f);
       if (lane < a.cs)
         asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(part.x), "=f"(part.y)
-                     : "r"(map_shared_rank(&s_part[i & 1], lane)) : "memory");
+                     : "r"(map_shared_rank(&s_part[turn], lane)) : "memory");
       m = warp_max(part.x);
       S = warp_sum(part.y * fast_exp2((part.x - m) * LOG2E));
     }
@@ -396,41 +412,41 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     __syncthreads();
     if (!dlogits) continue;
     const float inv = s_inv * e.correction();
-    const auto grad = [&](int c, const uint4& u) {
+    // (the whole warp, its lanes' vectors one after the other; c of lane 0 decides)
+    const auto grad = [&](int c, bool in, const uint4& u) {
       float v[N];
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] = e(PolVec<T>::get(u, k)) * inv;
-      row.store(c, PolVec<T>::pack(v));
+      row.store(c, in, PolVec<T>::pack(v));
     };
     // what was not kept first, while it is still in L2; then the slots, each
-    // refilled from the next row as its gradient leaves
-    for (int c = c_rest; c < c_hi; c += POL_THREADS) grad(c, row.load(c));
+    // refilled from the next row as its gradient leaves.  (Lane 0 has the most
+    // slots; the stores of ALIGNED need no other lane.)
+    for (int c = c_rest; ALIGNED ? c < c_hi : c - lane < c_hi; c += POL_THREADS)
+      grad(c, c < c_hi, c < c_hi ? row.load(c) : make_uint4(0, 0, 0, 0));
     const PolicyIn& in = s_in[(i + 1) & 1];
     have = i + 1 < end && in.w != 0.f && in.y >= 0 && in.y < a.V;
     if constexpr (ALIGNED) {
-      const T* shift = logits + (long long)(i + 1) * a.ld;
-      const Row next(shift, dlogits, a.V);  // (the vectors lie alike in every row)
+      const Row next(logits + (long long)(i + 1) * a.ld, nullptr, a.V);  // (its vectors lie alike)
 #pragma unroll 2
       for (int j = 0; j < kept; ++j) {
-        grad(c_lo + j * POL_THREADS, slot[j * POL_THREADS]);
+        grad(c_lo + j * POL_THREADS, true, slot[j * POL_THREADS]);
         if (have) copy(j, next, c_lo + j * POL_THREADS);
       }
     } else {
       const Row next = view(have ? i + 1 : i);
       const int n_lo = lo(next) + tid, n_hi = have ? hi(next) : n_lo;
-      for (int j0 = 0; j0 < POL_KEEP; j0 += POL_BATCH) {
-        uint4 u[POL_BATCH];
-#pragma unroll
-        for (int q = 0; q < POL_BATCH; ++q)
-          if (j0 + q < POL_KEEP && n_lo + (j0 + q) * POL_THREADS < n_hi) u[q] = next.load(n_lo + (j0 + q) * POL_THREADS);
-#pragma unroll
-        for (int q = 0; q < POL_BATCH; ++q) {
-          if (j0 + q < kept) grad(c_lo + (j0 + q) * POL_THREADS, slot[(j0 + q) * POL_THREADS]);
-          if (j0 + q < POL_KEEP && n_lo + (j0 + q) * POL_THREADS < n_hi) slot[(j0 + q) * POL_THREADS] = u[q];
-        }
+      const int slots = __shfl_sync(0xffffffffu, kept, 0);
+      int j = 0;
+#pragma unroll 2
+      for (; j < slots; ++j) {
+        grad(c_lo + j * POL_THREADS, j < kept, slot[j * POL_THREADS]);
+        if (n_lo + j * POL_THREADS < n_hi) copy(j, next, n_lo + j * POL_THREADS);
       }
+      for (; j < POL_KEEP && n_lo + j * POL_THREADS < n_hi; ++j) copy(j, next, n_lo + j * POL_THREADS);
     }
-    // the action's own element, by the thread that wrote its vector
+    __syncwarp();  // (the vectors' stores come before the next one)
+    // the action's own element, by the lane whose vector it is in
     const int c_y = (y + row.p) / N;
     if (c_y >= c_lo && c_y < c_hi && (c_y - c_lo) % POL_THREADS == 0)
       row.dz[y] = from_f<T>(fmaf(e(za), inv, s_g));
