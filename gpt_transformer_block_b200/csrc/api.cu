@@ -1742,8 +1742,8 @@ SmemOnce g_smem_policy[4];
 template <class T, bool ALIGNED>
 int policy_rows(const T* z, T* dz, PolicyArgs a, int* parts, cudaStream_t st) {
   TRY(allow_smem(policy_rows_kernel<T, ALIGNED>, POL_SMEM, g_smem_policy[(sizeof(T) == 2) * 2 + ALIGNED]));
-  // CTAs per row: two if one does not hold it (2000 fp32 rows of 50257: 235 us,
-  // against 261 with one that takes the rest from L2 and 365 and 417 with three
+  // CTAs per row: two if one does not hold it (2000 fp32 rows of 50257: 206 us,
+  // against 249 with one that takes the rest from L2, and 255 and 291 with three
   // and four, which hold all but wait for one another); more when there are
   // fewer rows than CTAs, down to two vectors per thread (29 bf16 rows of
   // 32768: 8.8 us with 8, 9.7 with one)
@@ -1761,7 +1761,7 @@ template <class T>
 int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, int* parts, cudaStream_t st) {
   const T* z = static_cast<const T*>(logits);
   T* dz = static_cast<T*>(dlogits);
-  // rows on 16-byte boundaries need no cutting (8192 bf16 rows of 32768: 177 us,
+  // rows on 16-byte boundaries need no cutting (8192 bf16 rows of 32768: 180 us,
   // against 207 by the general form)
   constexpr int N = 16 / (int)sizeof(T);
   const bool aligned = aligned16(z) && a.ld % N == 0 && (!dz || (aligned16(dz) && a.ldd % N == 0));

@@ -17,7 +17,7 @@
 // back from L2 for the gradient.  A few rows, or long ones, are shared out over
 // the CTAs of a cluster.  The next row's asynchronous copies go out as the
 // gradient leaves, so that HBM stays busy through the reductions (three CTAs
-// per SM, 8192 bf16 rows of 32768 of which a third do not count: 177 us, 5.1
+// per SM, 8192 bf16 rows of 32768 of which a third do not count: 180 us, 5.0
 // TB/s; the exponentials, two per element, take about 0.55 of the time on their
 // unit, which the loads have to overlap with).  The row's few scalars, loaded a
 // row ahead, are worked out in double by one warp (the ratio is held against
@@ -25,7 +25,7 @@
 // Vectors of 16 bytes are cut at the logits' alignment, row by row; where the
 // gradient's row lies otherwise, each 16-byte store is put together from a
 // lane's vector and the next lane's, so an odd vocabulary streams like an even
-// one (2000 fp32 rows of 50257, gradient rows without padding: ODD_NOTE us;
+// one (2000 fp32 rows of 50257, gradient rows without padding: 206 us, 3.7 TB/s;
 // with loads put together from two neighbours instead, through registers, 236).
 #pragma once
 #include <cfloat>
