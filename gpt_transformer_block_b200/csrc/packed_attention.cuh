@@ -817,12 +817,13 @@ __global__ void __launch_bounds__(256)
   if (blockIdx.x == 0) packed_check(cu, n_seq, total);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int STEP = 8, AHEAD = 4;
-  if ((int)blockIdx.x < few_ctas) {
+  const int few = (int)blockIdx.x - ((int)gridDim.x - few_ctas);  // (the last CTAs)
+  if (few >= 0) {
     // the rows that see few keys: the first ones of every sequence, or all
     const bool every = window >= 0 && window < PB_FEW;
     const long long items = (every ? (long long)n_rows : (long long)n_seq * PB_FEW) * H;
 #pragma unroll 1
-    for (long long i = (long long)blockIdx.x * STEP + warp; i < items; i += (long long)few_ctas * STEP) {
+    for (long long i = (long long)few * STEP + warp; i < items; i += (long long)few_ctas * STEP) {
       const int x = (int)(i / H), h = (int)(i - (long long)x * H);
       int t, first;
       if (every) {
@@ -850,7 +851,7 @@ __global__ void __launch_bounds__(256)
     }
     return;
   }
-  const int r0 = ((int)blockIdx.x - few_ctas) * rows;
+  const int r0 = (int)blockIdx.x * rows;
   if (r0 >= n_rows) return;
   if (threadIdx.x < rows && r0 + (int)threadIdx.x < n_rows) {
     const int t = r0 + threadIdx.x, first = packed_seq(cu, n_seq, t, n_rows).x;

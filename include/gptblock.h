@@ -390,8 +390,8 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
  * Offsets that break the order above are reported by gptb_device_error()
  * (GPTB_ERR_BAD_INPUT); the outputs are then undefined, and nothing outside
  * the arrays is touched.
- * Errors: GPTB_ERR_INVALID_ARG (null or misaligned pointers, strides, shapes),
- * GPTB_ERR_UNSUPPORTED (not an sm_100 device, total > 2^30). */
+ * Errors: GPTB_ERR_INVALID_ARG (null or misaligned pointers, strides, shapes,
+ * total > 2^30, n_seq > 2^26), GPTB_ERR_UNSUPPORTED (not an sm_100 device). */
 int gptb_packed_attention(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
                           const int32_t* cu_seqlens, void* o, long long ldo, float* lse, int total, int n_seq, int H,
                           int Hkv, int window, gptb_stream_t stream);
@@ -435,7 +435,9 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
  * Cache rows from lens[b] on and prefix rows of other groups reach no result,
  * whatever they hold.  Results do not vary from run to run.
  * Errors as for gptb_packed_attention; GPTB_ERR_WORKSPACE (too small),
- * GPTB_ERR_UNSUPPORTED (more than 128 query heads per kv head). */
+ * GPTB_ERR_UNSUPPORTED (more than 128 query heads per kv head; more than 2^30
+ * prefix or cache rows; B*Hkv times the 128-row tiles of T_max and total_prefix
+ * above 2^26). */
 size_t gptb_prefix_decode_workspace_bytes(int B, int H, int Hkv);
 int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void* v_prefix, long long ld_prefix,
                                  const int32_t* cu_prefix, int total_prefix, const int32_t* cu_group, int n_groups,
@@ -468,8 +470,8 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
  *            aligned
  * The only entry points that take pointers of less than 16-byte alignment
  * (logits, dlogits and the per-row arrays).  Results do not vary from run to
- * run.  Errors: GPTB_ERR_INVALID_ARG, GPTB_ERR_UNSUPPORTED (dtype),
- * GPTB_ERR_WORKSPACE. */
+ * run.  Errors: GPTB_ERR_INVALID_ARG (shapes, strides, clip borders, beta; more
+ * than 2^29 rows), GPTB_ERR_UNSUPPORTED (dtype), GPTB_ERR_WORKSPACE. */
 size_t gptb_policy_loss_workspace_bytes(int rows);
 int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
                      const float* weights, const float* advantages, const float* logp_old, const float* logp_ref,
