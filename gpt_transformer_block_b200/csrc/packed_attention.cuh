@@ -787,7 +787,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
 // 1 / sqrt(visible keys).  So for rows that see at most PB_FEW keys D is taken
 // as the sum of P dP, which needs no o: two lanes per key, by CTAs of their own.  (Without it dq and
 // dk of 5 sequences of 12 to 180 tokens were 2.6e-3 off in the norm, with it
-// 2.4e-3; 1.7e-3 is the rounding of the result alone.)
+// 2.4e-3; 1.7e-3 is the rounding of the result alone.  14600 rows of 12 heads: 44
+// us, 33 without the rows of few keys.)
 constexpr int PB_FEW = 16;
 constexpr int PB_PRE_ROWS = 16;  // most rows of a CTA
 
@@ -887,7 +888,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// after it: dQ rounded to bf16, 8 columns per thread
+// After it: dQ rounded to bf16, 8 columns per thread; bound by HBM (6 bytes per
+// element: 14600 rows of 12 heads in 20 us, 6.7 TB/s, some of it still in L2).
 __global__ void __launch_bounds__(256)
     packed_attn_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long lddq,
                           const int32_t* __restrict__ cu, int n_seq, int total, int H) {

@@ -30,7 +30,9 @@
 // for the V stage before it: 2600 cycles per tile); and the query rows of
 // several segments lie in shared memory side by side: the matrix product reads
 // 128 rows from the first of them on, and what lies behind makes rows of S that
-// nobody reads.
+// nobody reads.  64 samples over 32000 shared tokens, 12 heads, 10 to 250 own
+// tokens: 62 us with the join, 3.6 TB/s over all and 5 TB/s between start (3 us)
+// and join (8 us); 128 samples of 8 prompts, 10 heads over 5: 43 us.
 #pragma once
 #include "attention_tc.cuh"
 #include "common.cuh"
