@@ -194,15 +194,23 @@ __device__ __forceinline__ void policy_wait() { asm volatile("cp.async.wait_all;
 // exp(z - m) as exp2(z L - M), one fused operation and the exponential: M is
 // m L rounded to fp32, and the sum of such exponentials times correction() is
 // the sum of exp(z - m).  The product is exact inside the fused operation and
-// the difference is small where it counts, so large logits lose no digits.
-// Past 1e38 (rows whose logits are all the type's lowest) L is small enough for
-// M to be finite; there two different logits differ by 2^100 and more.
+// the difference is small where it counts, so no digits are lost -- as long as
+// M's rounding error, by which every exponent is off, is small itself: for |m|
+// up to POL_FAR it is at most 2^-4.  (Past 3e9 it can be 128, where exp2 of it
+// is infinite and that of its opposite 0.)  So a thread's maximum starts at
+// -POL_FAR, which a strip masked with a large value never leaves, and a row
+// whose maximum lies outside is done over with policy_far().
+constexpr float POL_FAR = 0x1p20f;
 struct PolicyExp {
-  float l, ml, m;
-  __device__ __forceinline__ explicit PolicyExp(float m_) : l(fabsf(m_) > 1e38f ? 0x1p-20f : LOG2E), ml(m_ * l), m(m_) {}
-  __device__ __forceinline__ float operator()(float z) const { return fast_exp2(fmaf(z, l, -ml)); }
-  __device__ __forceinline__ float correction() const { return fast_exp2(-fmaf(m, l, -ml)); }
+  float ml, m;
+  __device__ __forceinline__ explicit PolicyExp(float m_) : ml(m_ * LOG2E), m(m_) {}
+  __device__ __forceinline__ float operator()(float z) const { return fast_exp2(fmaf(z, LOG2E, -ml)); }
+  __device__ __forceinline__ float correction() const { return fast_exp2(-fmaf(m, LOG2E, -ml)); }
 };
+// The same from the difference: z - m is exact for z near m, and where it is
+// not the exponential is 0.  (One operation more per element: 2000 fp32 rows of
+// 50257 in 234 us where every vector chooses between the two forms, 214 so.)
+__device__ __forceinline__ float policy_far(float z, float m) { return fast_exp2((z - m) * LOG2E); }
 
 // what one warp works out for a row from its maximum m, sum s = sum exp(z - m)
 // and logit za: the log-probability, the gradient's coefficient g and the three sums
@@ -280,8 +288,8 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   using Row = PolicyRowView<T, ALIGNED>;
   extern __shared__ __align__(16) uint4 pol_slots[];  // [POL_KEEP][POL_THREADS]
   __shared__ float sm[POL_WARPS], ss[POL_WARPS];
-  // This CTA's maximum and sum of the row, in turn: a CTA may be a row ahead of
-  // those that still read its part of the last one, not two.
+  // This CTA's maximum and sum of the row, in turn: a CTA may be an exchange
+  // ahead of those that still read its part of the last one, not two.
   __shared__ float2 s_part[2];
   __shared__ float s_g, s_inv;
   __shared__ int s_scan[POL_WARPS], s_range[2];
@@ -321,7 +329,7 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
   }
   __syncthreads();
   bool have = false;  // the row is being loaded already
-  int turn = 0;       // of the rows that are read
+  int turn = 0;       // of the cluster's exchanges
   for (int i = first; i < end; ++i) {
     const Row row = view(i);
     const int c_lo = lo(row) + tid, c_hi = hi(row);
@@ -346,10 +354,9 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     if (!have) {
       for (int j = 0; j < kept; ++j) copy(j, row, c_lo + j * POL_THREADS);
     }
-    turn ^= 1;
     const float za = to_f(row.z[y]);
     // this thread's maximum and sum of exponentials, then the row's
-    float m = -FLT_MAX;  // (so that a strip of -inf adds 0)
+    float m = -POL_FAR;
     policy_wait();       // (this thread's copies)
 #pragma unroll 2
     for (int j = 0; j < kept; ++j) m = fmaxf(m, PolVec<T>::max(slot[j * POL_THREADS]));
@@ -374,27 +381,44 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
       }
       add(u);
     }
-    float s = ((s4[0] + s4[1]) + (s4[2] + s4[3])) * e.correction();
-    const float mw = warp_max(m);
-    s = warp_sum(s * fast_exp2((m - mw) * LOG2E));
-    if (lane == 0) {
-      sm[warp] = mw;
-      ss[warp] = s;
-    }
-    __syncthreads();
-    float m_lane = lane < POL_WARPS ? sm[lane] : -FLT_MAX;
-    m = warp_max(m_lane);
-    float S = 0.f;  // (warp 0)
-    if (warp == 0) S = warp_sum(lane < POL_WARPS ? ss[lane] * fast_exp2((m_lane - m) * LOG2E) : 0.f);
-    if (a.cs > 1) {  // the cluster's: each CTA reads the others' parts
-      if (tid == 0) s_part[turn] = make_float2(m, S);
-      cluster_sync_all();
-      float2 part = make_float2(-FLT_MAX, 0.f);
-      if (lane < a.cs)
-        asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(part.x), "=f"(part.y)
-                     : "r"(map_shared_rank(&s_part[turn], lane)) : "memory");
-      m = warp_max(part.x);
-      S = warp_sum(part.y * fast_exp2((part.x - m) * LOG2E));
+    // the row's, from every thread's maximum and sum; S in warp 0, with a cluster in all
+    float S = 0.f;
+    const auto join = [&](float s) {
+      const float mw = warp_max(m);
+      s = warp_sum(s * fast_exp2((m - mw) * LOG2E));
+      if (lane == 0) {
+        sm[warp] = mw;
+        ss[warp] = s;
+      }
+      __syncthreads();
+      const float m_lane = lane < POL_WARPS ? sm[lane] : -FLT_MAX;
+      m = warp_max(m_lane);
+      if (warp == 0) S = warp_sum(lane < POL_WARPS ? ss[lane] * fast_exp2((m_lane - m) * LOG2E) : 0.f);
+      if (a.cs > 1) {  // the cluster's: each CTA reads the others' parts
+        turn ^= 1;
+        if (tid == 0) s_part[turn] = make_float2(m, S);
+        cluster_sync_all();
+        float2 part = make_float2(-FLT_MAX, 0.f);
+        if (lane < a.cs)
+          asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(part.x), "=f"(part.y)
+                       : "r"(map_shared_rank(&s_part[turn], lane)) : "memory");
+        m = warp_max(part.x);
+        S = warp_sum(part.y * fast_exp2((part.x - m) * LOG2E));
+      }
+    };
+    join(((s4[0] + s4[1]) + (s4[2] + s4[3])) * e.correction());
+    const bool far = !(fabsf(m) < POL_FAR);  // (the same in the whole cluster)
+    if (far) {
+      m = -FLT_MAX;  // (so that a strip of -inf adds 0)
+      for (int c = c_lo; c < c_hi; c += POL_THREADS) m = fmaxf(m, PolVec<T>::max(row.load(c)));
+      s4[0] = s4[1] = s4[2] = s4[3] = 0.f;
+      for (int c = c_lo; c < c_hi; c += POL_THREADS) {
+        const uint4 u = row.load(c);
+#pragma unroll
+        for (int k = 0; k < N; ++k) s4[k & 3] += policy_far(PolVec<T>::get(u, k), m);
+      }
+      __syncthreads();  // (sm and ss have been read)
+      join((s4[0] + s4[1]) + (s4[2] + s4[3]));
     }
     e = PolicyExp(m);
     if (warp == 0) {
@@ -411,45 +435,56 @@ __global__ void __launch_bounds__(POL_THREADS, POL_CTAS)
     }
     __syncthreads();
     if (!dlogits) continue;
-    const float inv = s_inv * e.correction();
-    // (the whole warp, its lanes' vectors one after the other; c of lane 0 decides)
-    const auto grad = [&](int c, bool in, const uint4& u) {
-      float v[N];
+    const float inv = far ? s_inv : s_inv * e.correction();
+    if (far) {  // (no copies of the next row yet)
+      have = false;
+      for (int c = c_lo; c - lane < c_hi; c += POL_THREADS) {
+        const uint4 u = c < c_hi ? row.load(c) : make_uint4(0, 0, 0, 0);
+        float v[N];
 #pragma unroll
-      for (int k = 0; k < N; ++k) v[k] = e(PolVec<T>::get(u, k)) * inv;
-      row.store(c, in, PolVec<T>::pack(v));
-    };
-    // what was not kept first, while it is still in L2; then the slots, each
-    // refilled from the next row as its gradient leaves.  (Lane 0 has the most
-    // slots; the stores of ALIGNED need no other lane.)
-    for (int c = c_rest; ALIGNED ? c < c_hi : c - lane < c_hi; c += POL_THREADS)
-      grad(c, c < c_hi, c < c_hi ? row.load(c) : make_uint4(0, 0, 0, 0));
-    const PolicyIn& in = s_in[(i + 1) & 1];
-    have = i + 1 < end && in.w != 0.f && in.y >= 0 && in.y < a.V;
-    if constexpr (ALIGNED) {
-      const Row next(logits + (long long)(i + 1) * a.ld, nullptr, a.V);  // (its vectors lie alike)
-#pragma unroll 2
-      for (int j = 0; j < kept; ++j) {
-        grad(c_lo + j * POL_THREADS, true, slot[j * POL_THREADS]);
-        if (have) copy(j, next, c_lo + j * POL_THREADS);
+        for (int k = 0; k < N; ++k) v[k] = policy_far(PolVec<T>::get(u, k), m) * inv;
+        row.store(c, c < c_hi, PolVec<T>::pack(v));
       }
     } else {
-      const Row next = view(have ? i + 1 : i);
-      const int n_lo = lo(next) + tid, n_hi = have ? hi(next) : n_lo;
-      const int slots = __shfl_sync(0xffffffffu, kept, 0);
-      int j = 0;
+      // (the whole warp, its lanes' vectors one after the other; c of lane 0 decides)
+      const auto grad = [&](int c, bool in, const uint4& u) {
+        float v[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) v[k] = e(PolVec<T>::get(u, k)) * inv;
+        row.store(c, in, PolVec<T>::pack(v));
+      };
+      // what was not kept first, while it is still in L2; then the slots, each
+      // refilled from the next row as its gradient leaves.  (Lane 0 has the most
+      // slots; the stores of ALIGNED need no other lane.)
+      for (int c = c_rest; ALIGNED ? c < c_hi : c - lane < c_hi; c += POL_THREADS)
+        grad(c, c < c_hi, c < c_hi ? row.load(c) : make_uint4(0, 0, 0, 0));
+      const PolicyIn& in = s_in[(i + 1) & 1];
+      have = i + 1 < end && in.w != 0.f && in.y >= 0 && in.y < a.V;
+      if constexpr (ALIGNED) {
+        const Row next(logits + (long long)(i + 1) * a.ld, nullptr, a.V);  // (its vectors lie alike)
 #pragma unroll 2
-      for (; j < slots; ++j) {
-        grad(c_lo + j * POL_THREADS, j < kept, slot[j * POL_THREADS]);
-        if (n_lo + j * POL_THREADS < n_hi) copy(j, next, n_lo + j * POL_THREADS);
+        for (int j = 0; j < kept; ++j) {
+          grad(c_lo + j * POL_THREADS, true, slot[j * POL_THREADS]);
+          if (have) copy(j, next, c_lo + j * POL_THREADS);
+        }
+      } else {
+        const Row next = view(have ? i + 1 : i);
+        const int n_lo = lo(next) + tid, n_hi = have ? hi(next) : n_lo;
+        const int slots = __shfl_sync(0xffffffffu, kept, 0);
+        int j = 0;
+#pragma unroll 2
+        for (; j < slots; ++j) {
+          grad(c_lo + j * POL_THREADS, j < kept, slot[j * POL_THREADS]);
+          if (n_lo + j * POL_THREADS < n_hi) copy(j, next, n_lo + j * POL_THREADS);
+        }
+        for (; j < POL_KEEP && n_lo + j * POL_THREADS < n_hi; ++j) copy(j, next, n_lo + j * POL_THREADS);
       }
-      for (; j < POL_KEEP && n_lo + j * POL_THREADS < n_hi; ++j) copy(j, next, n_lo + j * POL_THREADS);
     }
     __syncwarp();  // (the vectors' stores come before the next one)
     // the action's own element, by the lane whose vector it is in
     const int c_y = (y + row.p) / N;
     if (c_y >= c_lo && c_y < c_hi && (c_y - c_lo) % POL_THREADS == 0)
-      row.dz[y] = from_f<T>(fmaf(e(za), inv, s_g));
+      row.dz[y] = from_f<T>(fmaf(far ? policy_far(za, m) : e(za), inv, s_g));
   }
   if (rank == 0 && tid < 3 && a.part) a.part[at * 3 + tid] = s_sum[tid];
   if (a.cs > 1) cluster_sync_all();  // no CTA leaves while another may read its part
