@@ -230,9 +230,11 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& a, const Polic
     const double plain = ratio * A;
     const double capped = fmin(fmax(ratio, 1.0 - (double)a.clip_lo), 1.0 + (double)a.clip_hi) * A;
     const bool kept = plain <= capped;
-    const double k = e - d - 1.0;
-    r.g = w * ((double)a.beta * (1.0 - e) - (kept ? plain : 0.0));
-    r.loss = w * ((double)a.beta * k - (kept ? plain : capped));
+    const double k = isinf(e) ? e : e - d - 1.0;  // (an action of probability 0: inf, not inf - inf)
+    const double beta = a.beta;
+    const bool term = beta != 0.0;  // (without the term e and k may be infinite)
+    r.g = w * ((term ? beta * (1.0 - e) : 0.0) - (kept ? plain : 0.0));
+    r.loss = w * ((term ? beta * k : 0.0) - (kept ? plain : capped));
     r.kl = w * k;
     r.clipped = kept ? 0.0 : w;
   }

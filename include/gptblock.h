@@ -465,7 +465,9 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
  *            themselves (ldd = ld then); NULL: no gradient
  *   logp:    device fp32 [rows]: lp
  *   stats:   device fp32 [3], overwritten: the loss, sum w (exp d - d - 1) and
- *            sum of w over the clipped rows (those without policy gradient)
+ *            sum of w over the clipped rows (those without policy gradient).
+ *            With beta = 0 and a logp_ref the second is computed all the same
+ *            and reaches neither the loss nor the gradient
  *   workspace: device, gptb_policy_loss_workspace_bytes(rows) bytes, 16-byte
  *            aligned
  * The only entry points that take pointers of less than 16-byte alignment

@@ -80,3 +80,25 @@ def test_close_logits_far_from_zero(cuda_lib, V, base):
     d["z"] = (base - step * k.double()).float()
     d["z"][torch.arange(3), d["a"].long()] = base
     check_all(cuda_lib, d)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("z_a", [-2000.0, float("-inf")])
+def test_reference_without_its_term(cuda_lib, dtype, z_a):
+    """beta 0 with a reference (the KL is only watched): an action that the policy has all but given up gives the loss,
+    the gradient and the clipped weight of a call without reference."""
+    gb = cuda_lib
+    d = policy_case(6, 700, dtype, seed=25, masked=0.0)
+    d["z"][2, d["a"][2].long()] = z_a
+    lp = torch.log_softmax(d["z"].double(), -1)[torch.arange(6), d["a"].long()]
+    d["old"] = (lp.clamp(min=-3000.0) + 0.05).float()
+    out = []
+    for ref in (d["ref"], None):
+        dz, logp, stats = torch.empty_like(d["z"]), torch.empty(6, device="cuda"), torch.empty(3, device="cuda")
+        ws = torch.empty(gb.gptb_policy_loss_workspace_bytes(6), dtype=torch.uint8, device="cuda")
+        gb.gptb_policy_loss(d["z"], d["a"], d["w"], d["A"], d["old"], ref, 0.2, 0.3, 0.0, dz, logp, stats, ws)
+        out.append((dz, logp, stats))
+    (dz, logp, stats), (dz0, logp0, stats0) = out
+    assert bool(torch.isfinite(dz).all()) and torch.equal(dz, dz0) and torch.equal(logp, logp0)
+    assert bool(torch.isfinite(stats[0])) and stats[0] == stats0[0] and stats[2] == stats0[2]
+    assert stats[1] == float("inf") and stats0[1] == 0
