@@ -7,9 +7,12 @@ BlockRunner one block's saved-activation and scratch workspaces for
 """
 from __future__ import annotations
 
+import contextlib
+import math
+
 import torch
 
-from . import (BF16, F32, WS_BLOCK_SAVED, WS_BLOCK_SCRATCH, WS_LM_HEAD, WS_STACK, block_grads,
+from . import (BF16, F32, WS_BLOCK_SAVED, WS_BLOCK_SCRATCH, WS_LM_HEAD, WS_STACK, _device, _flat, _rows, block_grads,
                block_weights, gpt_block_backward, gpt_block_forward, gpt_stack_step, gptb_gemm_bf16, gptb_policy_loss,
                gptb_policy_loss_workspace_bytes, gptb_token_logprobs, gptb_workspace_bytes, lm_head_xent, make_config,
                model_grads, model_weights)
@@ -114,21 +117,48 @@ def lm_head(c: dict, h, w_lm, targets, dh, dw_lm, stream=None):
     return loss
 
 
-def _logits(h, w_lm, out):
-    (n, d), V = h.shape, w_lm.shape[0]
-    gptb_gemm_bf16(h, 0, h.stride(0), w_lm, 0, d, out, 0, V, n, V, d)
+def _matrix(name: str, t, rows: int, cols: int, dtype, dev) -> int:
+    """The row stride of t, a [rows, cols] matrix as the GEMM takes it (contiguous rows, 16-byte boundaries)."""
+    if t.dim() != 2 or t.shape[1] != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, wanted [{rows}, {cols}]")
+    at, ld = _rows(name, t, cols, dtype, dev, rows)
+    if at % 16 or ld * t.element_size() % 16 or ld < cols:
+        raise ValueError(f"{name}: rows on 16-byte boundaries are wanted (address {at}, row stride {ld})")
+    return ld
+
+
+def _head(h, w_lm, rows_per_chunk):
+    """(device, rows, d, vocab, row strides of h and w_lm) of an lm_head over h."""
+    dev = _device("h", h)
+    if h.dim() != 2 or w_lm.dim() != 2:
+        raise ValueError(f"h, w_lm: matrices are wanted, not {tuple(h.shape)}, {tuple(w_lm.shape)}")
+    if rows_per_chunk < 1:
+        raise ValueError(f"rows_per_chunk: {rows_per_chunk}")
+    (N, d), V = h.shape, w_lm.shape[0]
+    if d % 8 or V % 8 or not d or not V:
+        raise ValueError(f"d and the vocabulary have to be multiples of 8, not {d}, {V}")
+    return dev, N, d, V, _matrix("h", h, N, d, torch.bfloat16, dev), _matrix("w_lm", w_lm, V, d, torch.bfloat16, dev)
+
+
+def _current(dev):
+    """dev as the current device, on whose current stream every launch of a call is made."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def lm_head_logprobs(h, w_lm, tokens, rows_per_chunk=8192):
-    """Log-probabilities [N] of the given tokens under logits h w_lm^T (bf16 h [N, d], w_lm [V, d]), a chunk of rows at
-    a time, on the current stream: what the sampling and the reference policy hand to lm_head_policy."""
-    N, V = h.shape[0], w_lm.shape[0]
-    logp = torch.empty(N, dtype=torch.float32, device=h.device)
-    z = torch.empty(min(N, rows_per_chunk), V, dtype=torch.bfloat16, device=h.device)
-    for i in range(0, N, rows_per_chunk):
-        n = min(rows_per_chunk, N - i)
-        _logits(h[i:i + n], w_lm, z[:n])
-        gptb_token_logprobs(z[:n], tokens[i:i + n], logp[i:i + n])
+    """Log-probabilities [N] of the given tokens (int32 [N]) under logits h w_lm^T (bf16 h [N, d], w_lm [V, d], column
+    ranges of wider arrays are fine; d and V multiples of 8), a chunk of rows at a time, on the current stream of the
+    tensors' device: what the sampling and the reference policy hand to lm_head_policy.  ValueError where an argument
+    does not fit, before anything is launched."""
+    dev, N, d, V, ldh, ldw = _head(h, w_lm, rows_per_chunk)
+    _flat("tokens", tokens, torch.int32, dev, N)
+    with _current(dev):
+        logp = torch.empty(N, dtype=torch.float32, device=dev)
+        z = torch.empty(min(N, rows_per_chunk), V, dtype=torch.bfloat16, device=dev)
+        for i in range(0, N, rows_per_chunk):
+            n = min(rows_per_chunk, N - i)
+            gptb_gemm_bf16(h[i:i + n], 0, ldh, w_lm, 0, ldw, z, 0, V, n, V, d)
+            gptb_token_logprobs(z[:n], tokens[i:i + n], logp[i:i + n])
     return logp
 
 
@@ -136,23 +166,34 @@ def lm_head_policy(h, w_lm, actions, weights, advantages, logp_old, logp_ref, cl
                    rows_per_chunk=8192):
     """The lm_head with the clipped policy loss in the place of the cross entropy: logits h w_lm^T of bf16 h [N, d] and
     w_lm [V, d] (d and V multiples of 8), gptb_policy_loss over them, and the gradients dh (bf16 [N, d], overwritten)
-    and dw_lm (fp32 [V, d], accumulated).  A chunk of rows at a time, the gradient over the logits, so the [N, V]
-    logits never exist whole; on the current stream.  Returns (stats [3]: loss, KL, clipped weight; logp [N])."""
-    (N, d), V = h.shape, w_lm.shape[0]
-    stats = torch.zeros(3, dtype=torch.float32, device=h.device)
-    logp = torch.empty(N, dtype=torch.float32, device=h.device)
-    part = torch.empty(3, dtype=torch.float32, device=h.device)
-    rows = max(1, min(N, rows_per_chunk))
-    z = torch.empty(rows, V, dtype=torch.bfloat16, device=h.device)
-    ws = _ws(gptb_policy_loss_workspace_bytes(rows), h.device)
-    for i in range(0, N, rows_per_chunk):
-        n, at = min(rows_per_chunk, N - i), slice(i, min(N, i + rows_per_chunk))
-        _logits(h[at], w_lm, z[:n])
-        gptb_policy_loss(z[:n], actions[at], weights[at], advantages[at], logp_old[at],
-                         None if logp_ref is None else logp_ref[at], clip_lo, clip_hi, beta, z[:n], logp[at], part, ws)
-        gptb_gemm_bf16(z, 0, V, w_lm, 1, d, dh[at], 0, dh.stride(0), n, d, V)
-        gptb_gemm_bf16(z, 1, V, h[at], 1, h.stride(0), dw_lm, 1, d, V, d, n)
-        stats += part
+    and dw_lm (fp32 [V, d], accumulated); the matrices may be column ranges of wider arrays.  A chunk of rows at a time,
+    the gradient over the logits, so the [N, V] logits never exist whole; on the current stream of the tensors' device.
+    Returns (stats [3]: loss, KL, clipped weight; logp [N]).  ValueError where an argument does not fit, before anything
+    is launched."""
+    dev, N, d, V, ldh, ldw = _head(h, w_lm, rows_per_chunk)
+    lddh = _matrix("dh", dh, N, d, torch.bfloat16, dev)
+    lddw = _matrix("dw_lm", dw_lm, V, d, torch.float32, dev)
+    _flat("actions", actions, torch.int32, dev, N)
+    for name, t in (("weights", weights), ("advantages", advantages), ("logp_old", logp_old), ("logp_ref", logp_ref)):
+        if t is not None or name != "logp_ref":
+            _flat(name, t, torch.float32, dev, N)
+    if not 0 <= clip_lo <= 1 or not clip_hi >= 0 or not math.isfinite(beta) or (beta and logp_ref is None):
+        raise ValueError(f"clip borders {clip_lo}, {clip_hi}, beta {beta} (with a beta logp_ref is needed)")
+    with _current(dev):
+        stats = torch.zeros(3, dtype=torch.float32, device=dev)
+        logp = torch.empty(N, dtype=torch.float32, device=dev)
+        part = torch.empty(3, dtype=torch.float32, device=dev)
+        rows = max(1, min(N, rows_per_chunk))
+        z = torch.empty(rows, V, dtype=torch.bfloat16, device=dev)
+        ws = _ws(gptb_policy_loss_workspace_bytes(rows), dev)
+        for i in range(0, N, rows_per_chunk):
+            n, at = min(rows_per_chunk, N - i), slice(i, min(N, i + rows_per_chunk))
+            gptb_gemm_bf16(h[at], 0, ldh, w_lm, 0, ldw, z, 0, V, n, V, d)
+            gptb_policy_loss(z[:n], actions[at], weights[at], advantages[at], logp_old[at],
+                             None if logp_ref is None else logp_ref[at], clip_lo, clip_hi, beta, z[:n], logp[at], part, ws)
+            gptb_gemm_bf16(z, 0, V, w_lm, 1, ldw, dh[at], 0, lddh, n, d, V)
+            gptb_gemm_bf16(z, 1, V, h[at], 1, ldh, dw_lm, 1, lddw, V, d, n)
+            stats += part
     return stats, logp
 
 
