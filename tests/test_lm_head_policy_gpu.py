@@ -59,3 +59,25 @@ def test_refused_before_any_launch(cuda_lib):
         assert torch.all(dh == 7.0) and torch.all(dw == 0)
     with pytest.raises(ValueError):
         run(x, dw=torch.zeros(V, D, dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("junk", [float("nan"), float("inf"), 3e38])
+def test_rows_without_weight_reach_no_gradient(cuda_lib, junk):
+    """Rows of weight 0 (prompt tokens, padding behind the last sequence, which packed attention leaves as it was) may
+    hold anything: dw and the other rows are those of a call with zeros there, dh is 0 in them."""
+    x = inputs(seed=1)
+    dead = torch.zeros(N, dtype=torch.bool, device="cuda")
+    dead[[0, 7, 130, N - 1]] = True
+    dead[200:260] = True
+    x["weights"][dead] = 0
+    clean, dirty = dict(x), dict(x)
+    clean["h"], dirty["h"] = x["h"].clone(), x["h"].clone()
+    clean["h"][dead], dirty["h"][dead] = 0, junk
+    for n in ("advantages", "logp_old", "logp_ref"):
+        dirty[n] = x[n].clone()
+        dirty[n][dead] = float("nan")
+    for chunk in (8192, 64):
+        want, got = run(clean, rows_per_chunk=chunk), run(dirty, rows_per_chunk=chunk)
+        assert bool(torch.isfinite(got[3]).all()) and torch.all(got[2][dead] == 0) and torch.all(got[1][dead] == 0)
+        same(got, want)
+    assert cuda_lib.gptb_device_error() == 0
