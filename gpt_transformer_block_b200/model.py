@@ -165,8 +165,8 @@ def lm_head_logprobs(h, w_lm, tokens, rows_per_chunk=8192):
 def lm_head_policy(h, w_lm, actions, weights, advantages, logp_old, logp_ref, clip_lo, clip_hi, beta, dh, dw_lm,
                    rows_per_chunk=8192):
     """The lm_head with the clipped policy loss in the place of the cross entropy: logits h w_lm^T of bf16 h [N, d] and
-    w_lm [V, d] (d and V multiples of 8), gptb_policy_loss over them, and the gradients dh (bf16 [N, d], overwritten)
-    and dw_lm (fp32 [V, d], accumulated); the matrices may be column ranges of wider arrays.  A chunk of rows at a time,
+    w_lm [V, d] (d and V multiples of 8), gptb_policy_loss over them, and the gradients dh (bf16 [N, d], overwritten; may
+    be h itself) and dw_lm (fp32 [V, d], accumulated); the matrices may be column ranges of wider arrays.  A chunk of rows at a time,
     the gradient over the logits, so the [N, V] logits never exist whole; on the current stream of the tensors' device.
     A row of weight 0 adds nothing, whatever its h and its other values are; its dh is 0.
     Returns (stats [3]: loss, KL, clipped weight; logp [N]).  ValueError where an argument does not fit, before anything
@@ -192,10 +192,10 @@ def lm_head_policy(h, w_lm, actions, weights, advantages, logp_old, logp_ref, cl
             gptb_gemm_bf16(h[at], 0, ldh, w_lm, 0, ldw, z, 0, V, n, V, d)
             gptb_policy_loss(z[:n], actions[at], weights[at], advantages[at], logp_old[at],
                              None if logp_ref is None else logp_ref[at], clip_lo, clip_hi, beta, z[:n], logp[at], part, ws)
-            gptb_gemm_bf16(z, 0, V, w_lm, 1, ldw, dh[at], 0, lddh, n, d, V)
             # (0 times a NaN is NaN: what a row of weight 0 holds must not meet the gradient's zeros)
             hw = torch.where((weights[at] != 0)[:, None], h[at], 0)
             gptb_gemm_bf16(z, 1, V, hw, 1, d, dw_lm, 1, lddw, V, d, n)
+            gptb_gemm_bf16(z, 0, V, w_lm, 1, ldw, dh[at], 0, lddh, n, d, V)
             stats += part
     return stats, logp
 

@@ -81,3 +81,13 @@ def test_rows_without_weight_reach_no_gradient(cuda_lib, junk):
         assert bool(torch.isfinite(got[3]).all()) and torch.all(got[2][dead] == 0) and torch.all(got[1][dead] == 0)
         same(got, want)
     assert cuda_lib.gptb_device_error() == 0
+
+
+def test_gradient_over_the_rows_themselves(cuda_lib):
+    """dh in the place of h: the same results, dw's product reads h first."""
+    x = inputs(seed=2)
+    x["weights"][::5] = 0
+    for chunk in (8192, 64):
+        want = run(x, rows_per_chunk=chunk)
+        y = dict(x, h=x["h"].clone())
+        same(run(y, dh=y["h"], rows_per_chunk=chunk), want)
