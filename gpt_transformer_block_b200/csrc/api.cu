@@ -191,6 +191,12 @@ bool make_tmap_3d(CUtensorMap* m, const void* ptr, bool f32, uint64_t inner, uin
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// arrays of int32 or fp32, each there and on an element's boundary
+template <class... P>
+bool words_ok(const P*... p) {
+  return (... && (p && aligned_to(p, 4)));
+}
 
 // cudaFuncAttributeMaxDynamicSharedMemorySize of a kernel, set once per device
 // (the call costs about as much host time as the launch itself)
@@ -1545,7 +1551,7 @@ bool packed_ok(const void* p, long long ld, int heads) {
   return p && aligned16(p) && ld % 8 == 0 && ld >= (long long)heads * 128 && ld < (1ll << 36);
 }
 bool packed_shape_ok(const int32_t* cu, int total, int n_seq, int H, int Hkv, int window) {
-  return cu && total >= 0 && total <= (1 << 30) && n_seq >= 0 && n_seq <= (1 << 26) && H > 0 && Hkv > 0 && H % Hkv == 0 && H <= (1 << 16) &&
+  return words_ok(cu) && total >= 0 && total <= (1 << 30) && n_seq >= 0 && n_seq <= (1 << 26) && H > 0 && Hkv > 0 && H % Hkv == 0 && H <= (1 << 16) &&
          window >= -1;
 }
 bool packed_map(CUtensorMap* m, const void* p, int heads, int total, long long ld, int box_rows) {
@@ -1560,7 +1566,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
                           int Hkv, int window, gptb_stream_t stream) {
   if (!packed_shape_ok(cu_seqlens, total, n_seq, H, Hkv, window)) return GPTB_ERR_INVALID_ARG;
   if (total == 0) return GPTB_OK;  // (empty arrays may have no address)
-  if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) || !lse)
+  if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) ||
+      !words_ok(lse))
     return GPTB_ERR_INVALID_ARG;
   const long long grid = (long long)((total + FA_BM - 1) / FA_BM) * H;
   if (grid > INT_MAX) return GPTB_ERR_UNSUPPORTED;
@@ -1591,7 +1598,7 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
   if (total == 0) return GPTB_OK;  // (empty arrays may have no address)
   if (!packed_ok(q, ldq, H) || !packed_ok(k, ldk, Hkv) || !packed_ok(v, ldv, Hkv) || !packed_ok(o, ldo, H) ||
       !packed_ok(dout, lddo, H) || !packed_ok(dq, lddq, H) || !packed_ok(dk, lddk, Hkv) || !packed_ok(dv, lddv, Hkv) ||
-      !lse || !workspace || !aligned16(workspace))
+      !words_ok(lse) || !workspace || !aligned16(workspace))
     return GPTB_ERR_INVALID_ARG;
   if (workspace_bytes < gptb_packed_attention_workspace_bytes(total, H)) return GPTB_ERR_WORKSPACE;
   const long long grid = (long long)((total + AB2_BK - 1) / AB2_BK) * Hkv;
@@ -1663,9 +1670,9 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
   if (B < 0 || H <= 0 || Hkv <= 0 || H % Hkv || T_max <= 0 || total_prefix < 0 || n_groups < 0 || window < -1)
     return GPTB_ERR_INVALID_ARG;
   if (B == 0) return GPTB_OK;  // (empty arrays may have no address)
-  if (!q || !k_cache || !v_cache || !lens || !o) return GPTB_ERR_INVALID_ARG;
+  if (!q || !k_cache || !v_cache || !o || !words_ok(lens) || !aligned_to(lse, 4)) return GPTB_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o)) return GPTB_ERR_INVALID_ARG;
-  if (n_groups > 0 && (!cu_prefix || !cu_group)) return GPTB_ERR_INVALID_ARG;
+  if (n_groups > 0 && !words_ok(cu_prefix, cu_group)) return GPTB_ERR_INVALID_ARG;
   if (n_groups > 0 && total_prefix > 0 && (!packed_ok(k_prefix, ld_prefix, Hkv) || !packed_ok(v_prefix, ld_prefix, Hkv)))
     return GPTB_ERR_INVALID_ARG;
   if (H / Hkv > 128) return GPTB_ERR_UNSUPPORTED;
@@ -1767,7 +1774,6 @@ int policy_launch(const void* logits, void* dlogits, const PolicyArgs& a, int* p
   const bool aligned = aligned16(z) && a.ld % N == 0 && (!dz || (aligned16(dz) && a.ldd % N == 0));
   return aligned ? policy_rows<T, true>(z, dz, a, parts, st) : policy_rows<T, false>(z, dz, a, parts, st);
 }
-bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 int policy_shape(const void* logits, long long ld, int dtype, int rows, int vocab) {
   if (dtype != GPTB_F32 && dtype != GPTB_BF16) return GPTB_ERR_UNSUPPORTED;
   if (rows < 0 || rows > (1 << 29) || vocab < 1 || vocab > (1 << 30) || ld < vocab || ld >= (1ll << 36)) return GPTB_ERR_INVALID_ARG;
@@ -1791,8 +1797,9 @@ int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int 
                      void* workspace, size_t workspace_bytes, gptb_stream_t stream) {
   TRY(policy_shape(logits, ld, dtype, rows, vocab));
   if (!(clip_lo >= 0.f && clip_lo <= 1.f) || !(clip_hi >= 0.f) || !std::isfinite(beta)) return GPTB_ERR_INVALID_ARG;
-  if (!stats) return GPTB_ERR_INVALID_ARG;
-  if (rows > 0 && (!actions || !weights || !advantages || !logp_old || !logp || (beta != 0.f && !logp_ref)))
+  if (!words_ok(stats)) return GPTB_ERR_INVALID_ARG;
+  if (rows > 0 && (!words_ok(actions, weights, advantages, logp_old, logp) || !aligned_to(logp_ref, 4) ||
+                   (beta != 0.f && !logp_ref)))
     return GPTB_ERR_INVALID_ARG;
   if (dlogits && (ldd < vocab || ldd >= (1ll << 36) || !aligned_to(dlogits, dtype == GPTB_F32 ? 4 : 2) ||
                   (dlogits == logits && ldd != ld)))
@@ -1818,7 +1825,7 @@ int gptb_token_logprobs(const void* logits, long long ld, int dtype, int rows, i
                         float* logp, gptb_stream_t stream) {
   TRY(policy_shape(logits, ld, dtype, rows, vocab));
   if (rows == 0) return GPTB_OK;
-  if (!tokens || !logp) return GPTB_ERR_INVALID_ARG;
+  if (!words_ok(tokens, logp)) return GPTB_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   PolicyArgs a{tokens, nullptr, nullptr, nullptr, nullptr, 0.f, 0.f, 0.f, logp, nullptr, ld, 0, rows, vocab, 1};
   int parts = 0;

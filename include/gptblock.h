@@ -390,6 +390,8 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
  * Offsets that break the order above are reported by gptb_device_error()
  * (GPTB_ERR_BAD_INPUT); the outputs are then undefined, and nothing outside
  * the arrays is touched.
+ * cu_seqlens and lse need their elements' alignment only (as do the int32 and
+ * fp32 arrays of the entry points below).
  * Errors: GPTB_ERR_INVALID_ARG (null or misaligned pointers, strides, shapes,
  * total > 2^30, n_seq > 2^26), GPTB_ERR_UNSUPPORTED (not an sm_100 device). */
 int gptb_packed_attention(const void* q, long long ldq, const void* k, long long ldk, const void* v, long long ldv,
@@ -470,9 +472,8 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
  *            and reaches neither the loss nor the gradient
  *   workspace: device, gptb_policy_loss_workspace_bytes(rows) bytes, 16-byte
  *            aligned
- * The only entry points that take pointers of less than 16-byte alignment
- * (logits, dlogits and the per-row arrays).  Results do not vary from run to
- * run.  Errors: GPTB_ERR_INVALID_ARG (shapes, strides, clip borders, beta; more
+ * logits, dlogits and the per-row arrays need their elements' alignment only.
+ * Results do not vary from run to run.  Errors: GPTB_ERR_INVALID_ARG (shapes, strides, clip borders, beta; more
  * than 2^29 rows), GPTB_ERR_UNSUPPORTED (dtype), GPTB_ERR_WORKSPACE. */
 size_t gptb_policy_loss_workspace_bytes(int rows);
 int gptb_policy_loss(const void* logits, long long ld, int dtype, int rows, int vocab, const int32_t* actions,
