@@ -406,9 +406,19 @@ def _device(name: str, t):
     return dev
 
 
+_INT_MAX = 2 ** 31 - 1  # (ctypes cuts what a C int does not hold, without a word)
+
+
+def _window(w) -> int:
+    """A window for the C entry points: all rows of any array lie within the largest one."""
+    return max(-2, min(int(w), _INT_MAX))
+
+
 def _rows(name: str, t, cols: int, dtype, device, rows):
     """t as a [rows, >= cols] matrix whose rows are contiguous: (address, row stride)."""
     shape, stride = t.shape, t.stride()
+    if rows > _INT_MAX or cols > _INT_MAX:
+        raise ValueError(f"{name}: [{rows}, {cols}] has 2**31 or more rows or columns")
     if len(shape) != 2 or shape[0] != rows or shape[1] < cols:
         raise ValueError(f"{name}: shape {tuple(shape)}, wanted [{rows}, {cols}]")
     if stride[1] != 1 and shape[1] > 1:
@@ -457,7 +467,7 @@ def gptb_packed_attention(q, k, v, cu_seqlens, o, lse, H, Hkv, window=-1, stream
     args = (*_rows("q", q, H * 128, bf, dev, n), *_rows("k", k, Hkv * 128, bf, dev, n),
             *_rows("v", v, Hkv * 128, bf, dev, n), _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
             *_rows("o", o, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n), n,
-            cu_seqlens.numel() - 1, H, Hkv, int(window))
+            cu_seqlens.numel() - 1, H, Hkv, _window(window))
     _enqueue(dev, load().gptb_packed_attention, args, stream, "gptb_packed_attention")
 
 
@@ -475,7 +485,7 @@ def gptb_packed_attention_backward(q, k, v, o, dout, lse, cu_seqlens, dq, dk, dv
             *_rows("dout", dout, H * 128, bf, dev, n), _flat("lse", lse, torch.float32, dev, H * n),
             _flat("cu_seqlens", cu_seqlens, torch.int32, dev, cu_seqlens.numel()),
             *_rows("dq", dq, H * 128, bf, dev, n), *_rows("dk", dk, Hkv * 128, bf, dev, n),
-            *_rows("dv", dv, Hkv * 128, bf, dev, n), n, cu_seqlens.numel() - 1, H, Hkv, int(window),
+            *_rows("dv", dv, Hkv * 128, bf, dev, n), n, cu_seqlens.numel() - 1, H, Hkv, _window(window),
             *_workspace(workspace, dev))
     _enqueue(dev, load().gptb_packed_attention_backward, args, stream, "gptb_packed_attention_backward")
 
@@ -500,7 +510,7 @@ def gptb_prefix_decode_attention(q, k_prefix, v_prefix, cu_prefix, cu_group, k_c
             _flat("cu_group", cu_group, i32, dev, n), max(0, n - 1),
             _flat("k_cache", k_cache, bf, dev, B * T * Hkv * 128), _flat("v_cache", v_cache, bf, dev, B * T * Hkv * 128),
             _flat("lens", lens, i32, dev, B), T, _flat("o", o, bf, dev, B * H * 128),
-            None if lse is None else _flat("lse", lse, torch.float32, dev, B * H), B, H, Hkv, int(window),
+            None if lse is None else _flat("lse", lse, torch.float32, dev, B * H), B, H, Hkv, _window(window),
             *_workspace(workspace, dev))
     _enqueue(dev, load().gptb_prefix_decode_attention, args, stream, "gptb_prefix_decode_attention")
 
