@@ -1579,7 +1579,9 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
     return GPTB_ERR_CUDA;
   TRY(allow_smem(packed_attn_fwd_kernel, PF_SMEM, g_smem_packed_fwd));
   packed_attn_fwd_kernel<<<(unsigned)grid, PF_THREADS, PF_SMEM, reinterpret_cast<cudaStream_t>(stream)>>>(
-      tq, tk, tv, to, static_cast<bf16*>(o), ldo, lse, cu_seqlens, n_seq, total, H, Hkv, window);
+      tq, tk, tv, to,
+      PackedRows{static_cast<const bf16*>(q), static_cast<const bf16*>(k), static_cast<const bf16*>(v), ldq, ldk, ldv},
+      static_cast<bf16*>(o), ldo, lse, cu_seqlens, n_seq, total, H, Hkv, window);
   CKL();
   return GPTB_OK;
 }

@@ -13,9 +13,11 @@
 // own visible range, and only the tiles that some row sees are visited.  So
 // the grid needs neither the lengths nor a plan made from them (they stay on
 // the device), and short sequences share tiles instead of padding one each.
-// Products with P = 0 are part of the matrix products, so a NaN or infinity in
-// a row reaches the rows that share a tile with it; what lies behind the last
-// sequence reaches nothing.
+// Products with P = 0 are part of the matrix products, and 0 * NaN is NaN.  What
+// lies behind the last sequence is zeroed on the way; in the forward a row whose
+// result is not finite is worked out again from the rows that it sees, so no
+// row's NaN or infinity reaches one that does not see it.  (The backward takes
+// finite rows only.)
 //
 // The tile schedules are those of attention_tc.cuh: forward 256 queries of one
 // head per CTA over 128-key tiles, backward 128 keys of one kv head per CTA
@@ -58,6 +60,72 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
     *reinterpret_cast<uint4*>(tile + (c >> 3) * half + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
 }
 
+// q, k and v as rows, for what the tensor cores cannot be asked
+struct PackedRows {
+  const bf16 *q, *k, *v;
+  long long ldq, ldk, ldv;
+};
+
+// The rows of `again` (a bit per lane; the lane has row row0 + lane's first
+// visible key, maximum and inverse sum) once more, by the warp from the rows
+// that they see: o = sum of exp2(s - m) inv v, s in base 2, 4 columns per lane,
+// in the columns that are not finite at `at` (row 0, `pitch` bytes from row to
+// row; or, pitch 0, the swizzled tile).  From the newest key back, until all of
+// those columns are not finite again: nothing makes them so any more.
+__device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_lo, float m_used, float inv_l,
+                                               const bf16* q, long long ldq, const bf16* k, long long ldk, const bf16* v,
+                                               long long ldv, uint8_t* at0, long long pitch) {
+  const int lane = threadIdx.x & 31, c = lane * 4;
+  const auto four = [](const uint2& u, float (&x)[4]) {
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xffff0000u);
+  };
+  const auto load4 = [&](const bf16* p, float (&x)[4]) { four(*reinterpret_cast<const uint2*>(p + c), x); };
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int x = __ffs(again) - 1, t = row0 + x;
+    const int lo = __shfl_sync(0xffffffffu, kv_lo, x);
+    const float m = __shfl_sync(0xffffffffu, m_used, x), inv = __shfl_sync(0xffffffffu, inv_l, x);
+    uint2* at = reinterpret_cast<uint2*>(
+        pitch ? at0 + x * pitch + lane * 8
+              : at0 + (lane >> 4) * 16384 + x * 128 + ((((lane & 15) >> 1) ^ (x & 7)) << 4) + (lane & 1) * 8);
+    float old[4], a[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+    four(*at, old);
+    bool open = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) open |= !(fabsf(old[i]) < INFINITY);
+    load4(q + t * ldq, a);
+#pragma unroll 1
+    for (int j0 = t; j0 >= lo && __any_sync(0xffffffffu, open); j0 -= 4) {
+      float s[4], y[4][4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const long long j = max(j0 - e, lo);
+        float b[4];
+        load4(k + j * ldk, b);
+        load4(v + j * ldv, y[e]);
+        s[e] = fmaf(a[0], b[0], fmaf(a[1], b[1], fmaf(a[2], b[2], a[3] * b[3])));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = warp_sum(s[e]);
+        if (j0 - e < lo) continue;
+        const float p = fast_exp2(fmaf(s[e], LOG2E / sqrtf(128.f), -m)) * inv;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(p, y[e][i], acc[i]);
+      }
+      open = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) open |= !(fabsf(old[i]) < INFINITY) && fabsf(acc[i]) < INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) old[i] = fabsf(old[i]) < INFINITY ? old[i] : acc[i];
+    *at = make_uint2(pack_bf16(old[0], old[1]), pack_bf16(old[2], old[3]));
+  }
+}
+
 // Forward.  CTA = 128 consecutive packed rows of one head, two CTAs per SM, 6
 // warps: 0 TMA producer (Q once; K and V tiles of 64 keys, two stages each), 1
 // TMEM owner and MMA issuer, 2-5 softmax (thread = query row, its TMEM lane).
@@ -75,13 +143,14 @@ __device__ __forceinline__ void zero_tile_row(uint8_t* tile, int half, int r) {
 // (attention_tc.cuh) 220 and 84.
 constexpr int PF_THREADS = 192;
 constexpr int PF_BN = 64;
+constexpr int PF_LONG = 32;                                // key tiles, 2048 keys
 constexpr int PF_KV = PF_BN * 128 * 2;                     // one K or V tile: two 64-column swizzled halves of 8 KB
 constexpr int PF_SMEM = 1024 + FA_TILE /*Q*/ + 4 * PF_KV;  // K, V x2
 
 __global__ void __launch_bounds__(PF_THREADS, 2)
     packed_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
-                           bf16* __restrict__ o, long long ldo, float* __restrict__ lse,
+                           const PackedRows in, bf16* __restrict__ o, long long ldo, float* __restrict__ lse,
                            const int32_t* __restrict__ cu, int n_seq, int total, int H, int Hkv, int window) {
   extern __shared__ uint8_t fa_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fa_smem_raw) + 1023) & ~uintptr_t(1023));
@@ -218,6 +287,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
     const int r = qw * 32 + lane;  // row within the query tile
     const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
     const float sl2 = LOG2E / sqrtf(128.f);
+    const int lo = s_lo;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     for (int c = 0; c < n && ok; ++c) {
@@ -279,12 +349,16 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       float l0, l1;
       f2_unpack(f2_add(lp[0], lp[1]), l0, l1);
       l += l0 + l1;
-      // V rows behind the last sequence may hold anything (0 * NaN is NaN):
-      // they are zeroed before the product that reads them
-      if (n_rows < total && k0 + PF_BN > n_rows) {
+      // V rows that no query of this CTA sees may hold anything (0 * NaN is NaN).
+      // Those behind the last sequence are zeroed before the product that reads
+      // them, those before the first query's range where a CTA has many key
+      // tiles: else a NaN before a long sequence would send all of it through
+      // packed_rows_alone().  (For few tiles that is cheap, and the zeroing
+      // is not: 512 sequences of 24 rows, 12 heads, 50 us with it, 47 without.)
+      if ((n_rows < total && k0 + PF_BN > n_rows) || (n > PF_LONG && k0 < lo)) {
         ok = mbar_wait_warp(&v_full[st], (c >> 1) & 1, abort_flag, ERRW_TIMEOUT_EPILOGUE);
         if (!ok) break;
-        if (r < PF_BN && k0 + r >= n_rows) zero_tile_row(sV + st * PF_KV, 8192, r);
+        if (r < PF_BN && (k0 + r >= n_rows || k0 + r < lo)) zero_tile_row(sV + st * PF_KV, 8192, r);
         fence_proxy_async_smem();
       }
       // O to the new max, once it holds every PV product up to tile c-1 (the
@@ -320,12 +394,15 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       // rows go out one by one
       const int row0 = q0 + qw * 32;  // first query of this warp's rows
       const bool whole = row0 + 32 <= n_rows;
+      f32x2 all = 0;  // the sum of the row's O: finite unless one of them is not (or they are as large as that)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {  // columns 32k .. 32k+31
         uint32_t w[32];
         tmem_ld_32x32b_x32(lane_addr + 128 + k * 32, w);
         tmem_ld_wait();
         uint8_t* row = sQ + (k >> 1) * 16384 + r * 128;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) all = f2_add(all, f2_pack(__uint_as_float(w[i]), __uint_as_float(w[i + 1])));
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           uint4 u;
@@ -340,6 +417,17 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
             *reinterpret_cast<uint4*>(o + (long long)tq * ldo + h * 128 + k * 32 + g * 8) = u;
         }
       }
+      // A row whose o is not finite may owe that to rows it does not see (P = 0
+      // there, and 0 * NaN is NaN), so it is worked out again from those that it
+      // sees
+      float a0, a1;
+      f2_unpack(all, a0, a1);
+      __syncwarp();
+      const unsigned again = __ballot_sync(0xffffffffu, tq < n_rows && !(fabsf(a0 + a1) < INFINITY));
+      if (again)
+        packed_rows_alone(again, row0, kv_lo, m_used, inv, in.q + h * 128, in.ldq, in.k + kvh * 128, in.ldk, in.v + kvh * 128,
+                          in.ldv, whole ? sQ + qw * 4096 : reinterpret_cast<uint8_t*>(o + row0 * ldo + h * 128),
+                          whole ? 0 : ldo * 2);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && whole) {

@@ -384,9 +384,9 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
  *   lse:     device fp32 [H, total] (natural log of the softmax denominator
  *            including its max)
  * Rows from cu[n_seq] on belong to no sequence: whatever they hold reaches no
- * result, and their outputs are left as they were.  Inside the sequences q, k,
- * v (and dout) have to be finite: rows share tiles, and a NaN or infinity can
- * reach the rows of a neighbouring sequence.  Outputs overlap no input.
+ * result, and their outputs are left as they were.  A NaN or infinity in a row
+ * of k or v reaches o (and one of k lse) of the rows that see it, one of q that
+ * of its own row, and nothing else.  Outputs overlap no input.
  * Offsets that break the order above are reported by gptb_device_error()
  * (GPTB_ERR_BAD_INPUT); the outputs are then undefined, and nothing outside
  * the arrays is touched.
@@ -400,6 +400,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
 
 /* Its backward pass: dq, dk, dv (bf16, overwritten, strided like q, k, v) from
  * dout (the gradient of o) and the o and lse that the forward call wrote.
+ * Inside the sequences q, k, v and dout have to be finite: a NaN or infinity can
+ * reach the gradients of rows that share a tile with it.
  *   workspace: device, gptb_packed_attention_workspace_bytes(total, H) bytes,
  *            16-byte aligned
  * dq is summed over key tiles by fp32 reductions whose order varies, so its
