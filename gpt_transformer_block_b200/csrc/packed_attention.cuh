@@ -13,11 +13,11 @@
 // own visible range, and only the tiles that some row sees are visited.  So
 // the grid needs neither the lengths nor a plan made from them (they stay on
 // the device), and short sequences share tiles instead of padding one each.
-// Products with P = 0 are part of the matrix products, and 0 * NaN is NaN.  What
-// lies behind the last sequence is zeroed on the way; in the forward a row whose
-// result is not finite is worked out again from the rows that it sees, so no
-// row's NaN or infinity reaches one that does not see it.  (The backward takes
-// finite rows only.)
+// Products with P = 0 are part of the matrix products, and 0 * NaN is NaN.  Rows
+// behind the last sequence are zeroed before them; so are, in the backward, rows
+// that are not finite, with P or dS made NaN for the pairs that are visible.  V
+// does not show itself in time, so in the forward a row whose result is not
+// finite is worked out again from the rows that it sees.
 //
 // The tile schedules are those of attention_tc.cuh: forward 256 queries of one
 // head per CTA over 128-key tiles, backward 128 keys of one kv head per CTA
@@ -66,6 +66,8 @@ struct PackedRows {
   long long ldq, ldk, ldv;
 };
 
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+
 // The rows of `again` (a bit per lane; the lane has row row0 + lane's first
 // visible key, maximum and inverse sum) once more, by the warp from the rows
 // that they see: o = sum of exp2(s - m) inv v, s in base 2, 4 columns per lane,
@@ -95,7 +97,7 @@ __device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_
     four(*at, old);
     bool open = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) open |= !(fabsf(old[i]) < INFINITY);
+    for (int i = 0; i < 4; ++i) open |= !finite(old[i]);
     load4(q + t * ldq, a);
 #pragma unroll 1
     for (int j0 = t; j0 >= lo && __any_sync(0xffffffffu, open); j0 -= 4) {
@@ -118,10 +120,10 @@ __device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_
       }
       open = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) open |= !(fabsf(old[i]) < INFINITY) && fabsf(acc[i]) < INFINITY;
+      for (int i = 0; i < 4; ++i) open |= !finite(old[i]) && finite(acc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) old[i] = fabsf(old[i]) < INFINITY ? old[i] : acc[i];
+    for (int i = 0; i < 4; ++i) old[i] = finite(old[i]) ? old[i] : acc[i];
     *at = make_uint2(pack_bf16(old[0], old[1]), pack_bf16(old[2], old[3]));
   }
 }
@@ -423,7 +425,7 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
       float a0, a1;
       f2_unpack(all, a0, a1);
       __syncwarp();
-      const unsigned again = __ballot_sync(0xffffffffu, tq < n_rows && !(fabsf(a0 + a1) < INFINITY));
+      const unsigned again = __ballot_sync(0xffffffffu, tq < n_rows && !finite(a0 + a1));
       if (again)
         packed_rows_alone(again, row0, kv_lo, m_used, inv, in.q + h * 128, in.ldq, in.k + kvh * 128, in.ldk, in.v + kvh * 128,
                           in.ldv, whole ? sQ + qw * 4096 : reinterpret_cast<uint8_t*>(o + row0 * ldo + h * 128),
@@ -448,6 +450,17 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
   }
 }
 
+// zeroes the Q and dO rows of a stage whose LSE is not finite (out of the way of the loop that calls it)
+__device__ __noinline__ void packed_zero_odd(uint8_t* q, uint8_t* dO, const float* lse) {
+#pragma unroll 1
+  for (int r = 0; r < AB2_BQ; ++r) {
+    if (finite(lse[r])) continue;
+    zero_tile_row(q, 8192, r);
+    zero_tile_row(dO, 8192, r);
+  }
+  fence_proxy_async_smem();
+}
+
 // Backward.  Roles, TMEM columns and barriers as in attn_bwd_tc_kernel: 128
 // keys of one kv head per CTA, a chain of steps of one query head and 64
 // queries each.  A chain costs 10 us to start and end and 2 us per step, so
@@ -455,6 +468,15 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
 // every CTA takes a part of its steps, and the partial dK and dV meet through
 // distributed shared memory, added in a fixed order (5 sequences of 12 to 180
 // tokens, 8 query heads over 2: 47 us with one CTA per chain, 30 with 8).
+//
+// A query whose LSE or D is not finite (its q or dout is not, or a k or v that
+// it sees) has P and dS of NaN where it sees a key: the producer makes its LSE
+// NaN, and the MMA warp zeroes its Q and dO rows before the products in which
+// they would meet the zeros of other keys.  A key whose row of K is not finite
+// is found by the dQ warps while they wait for the first step: they zero the row
+// and make that of V NaN, so that dS is NaN where a query sees the key.  None of
+// this is on the softmax warps' way: with the checks there, 20 sequences of 200
+// to 2048 rows take 575 us (forward and backward), so 541, and 535 without them.
 constexpr int PB_CLUSTER = 8;
 __global__ void __launch_bounds__(AB2_THREADS, 1)
     packed_attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -487,6 +509,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
   float* sLD = reinterpret_cast<float*>(bars + 32);  // [AB2_STAGES][lse*log2e 64 | D 64]
 
   __shared__ int s_vis[2];  // last query that sees the tile's first key; ... its last key
+  __shared__ int s_odd[AB2_STAGES];  // the stage has a query whose LSE or D is not finite
 
   const int rank = (int)blockIdx.x % cs, chain = (int)blockIdx.x / cs;
   const int kb = chain / Hkv, kvh = chain % Hkv;
@@ -581,13 +604,18 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
         tma_load_2d(d + 8192, &tm_do, &qdo_full[st], hh * 128 + 64, q0);
       }
       float* ld = sLD + st * 128;
+      bool odd = false;
       for (int e = lane; e < 64; e += 32) {
         const int t = q0 + e;
         const long long li = (long long)hh * total + t;
-        ld[e] = (t < n_rows) ? lse[li] * LOG2E : 0.f;
-        ld[64 + e] = (t < n_rows) ? Dd[li] : 0.f;
+        const float l2 = (t < n_rows) ? lse[li] * LOG2E : 0.f, d = (t < n_rows) ? Dd[li] : 0.f;
+        const bool here = !(finite(l2) && finite(d));
+        ld[e] = here ? NAN : l2;
+        ld[64 + e] = d;
+        odd |= here;
       }
-      __syncwarp();
+      odd = __any_sync(0xffffffffu, odd);
+      if (lane == 0) s_odd[st] = odd;
       if (lane == 0) mbar_arrive(&qdo_full[st]);
     }
   } else if (warp == 1) {
@@ -600,7 +628,9 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
       bool ok = mbar_wait(kv_full, 0, abort_flag, ERRW_TIMEOUT_MMA);
       auto grads = [&](int i) -> bool {
         const int st = i % AB2_STAGES;
+        const int odd = s_odd[st];
         if (!mbar_wait(p_full, i & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        if (odd) packed_zero_odd(sQ + st * AB2_Q_TILE, sDO + st * AB2_Q_TILE, sLD + st * 128);
         tc_fence_after();
         const uint32_t aQ = smem_u32(sQ + st * AB2_Q_TILE), aDO = smem_u32(sDO + st * AB2_Q_TILE);
 #pragma unroll
@@ -611,7 +641,7 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
           mma_bf16_ts(tmem + 128, tmem + 448 + k * 8, smem_desc_sw128(aDO + k * 2048, 8192, 1024), ID_G, acc);
           mma_bf16_ts(tmem + 0, tmem + 480 + k * 8, smem_desc_sw128(aQ + k * 2048, 8192, 1024), ID_G, acc);
         }
-        if (!mbar_wait(dq_free, (i & 1) ^ 1u, abort_flag, ERRW_TIMEOUT_MMA)) return false;
+        if (!mbar_wait(dq_free, i & 1, abort_flag, ERRW_TIMEOUT_MMA)) return false;  // (its first phase: K is in order)
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -793,7 +823,34 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
     const int qw = warp & 3;
     const int qh = (warp - 10) >> 2;  // queries qh*32 .. qh*32+31 of the tile
     const uint32_t lane_addr = tmem + ((uint32_t)(qw * 32) << 16);
-    bool ok = true;
+    bool ok = mbar_wait_warp(kv_full, 0, abort_flag, ERRW_TIMEOUT_EPILOGUE);
+    if (ok) {  // rows of K that are not finite: 16 rows per warp, half a row per lane
+      const int row = (warp - 10) * 16 + (lane & 15);
+      const auto chunk = [&](uint8_t* tile, int c) {
+        return reinterpret_cast<uint4*>(tile + (lane >> 4) * 16384 + row * 128 + ((c ^ (row & 7)) << 4));
+      };
+      uint32_t odd = 0;  // the exponent of a NaN or infinity is all ones: one more carries into the bit above
+      const auto look = [&](uint32_t u) { odd |= (u & 0x7f807f80u) + 0x00800080u; };
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const uint4 u = *chunk(sK, c);
+        look(u.x);
+        look(u.y);
+        look(u.z);
+        look(u.w);
+      }
+      odd |= __shfl_xor_sync(0xffffffffu, odd, 16);
+      if (odd & 0x80008000u) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          *chunk(sV, c) = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+          *chunk(sK, c) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(dq_free);
     for (int i = 0; i < steps; ++i) {
       const int hh = kvh * G + (first + i) / nq;
       const int q0 = (qt_lo + (first + i) % nq) * AB2_BQ;

@@ -400,8 +400,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
 
 /* Its backward pass: dq, dk, dv (bf16, overwritten, strided like q, k, v) from
  * dout (the gradient of o) and the o and lse that the forward call wrote.
- * Inside the sequences q, k, v and dout have to be finite: a NaN or infinity can
- * reach the gradients of rows that share a tile with it.
+ * A NaN or infinity in a row of q or dout, or of a k or v that the row sees,
+ * reaches the row's dq and the dk and dv of the keys that it sees, nothing else.
  *   workspace: device, gptb_packed_attention_workspace_bytes(total, H) bytes,
  *            16-byte aligned
  * dq is summed over key tiles by fp32 reductions whose order varies, so its

@@ -111,3 +111,57 @@ def test_a_long_sequence_after_a_spoilt_one(cuda_lib):
     want = orl.packed_attention(q, k, v, np.array([0, 2011]), -1)
     for got in (o, o_nan):
         within(heads(got[37:2048], H), want["o"], want["err"]["o"])
+
+
+D_SPOTS = [("d", 1, 0.5, 1, 7, float("nan")), ("d", 2, 0.0, None, None, float("inf")),
+           ("d", 3, 1.0, 0, 90, float("-inf")), ("d", 0, None, None, None, float("nan"))]
+CASES = [(batch, window, spot) for batch in sorted(BATCHES) for window in (-1, 0, 50) for spot in SPOTS + D_SPOTS]
+# (2 to 10 key tiles of 2 kv heads: clusters of 8 and 4 CTAs; 40 of them: no clusters)
+BATCHES["no clusters"] = [150, 700, 1, 4200, 64]
+CASES += [("no clusters", 50, spot) for spot in (SPOTS + D_SPOTS)[1::3]]
+
+
+@pytest.mark.parametrize("batch,window,spot", CASES, ids=lambda s: s if not isinstance(s, tuple) else f"{s[0]}{s[1]}-{s[2]}-{s[5]}")
+def test_backward(cuda_lib, batch, window, spot):
+    """A query is spoilt that sees a spoilt row, or whose own q or dout is; its dq, and dk and dv of the keys that it
+    sees, may be anything, every other gradient is that of the batch with zeros there."""
+    gb = cuda_lib
+    lens = BATCHES[batch]
+    for pad in (0, 21):
+        qkv, dout, cu = packed(lens, H, HK, seed=3, pad=pad)
+        cu_h = cu.cpu().numpy()
+        m, n = int(cu_h[-1]), len(qkv)
+        name, s, share, head, col, x = spot
+        d_bad, d_clean = dout.clone(), dout.clone()
+        if name == "d":
+            a, b = int(cu_h[s]), int(cu_h[s + 1])
+            rows = np.arange(a, b) if share is None else np.array([a + round((b - 1 - a) * share)])
+            kvs, bad, clean = range(HK) if head is None else [head], qkv, qkv
+            cols = slice(None) if col is None else slice(col, col + 1)
+            for kv in kvs:
+                for t, y in ((d_bad, x), (d_clean, 0.0)):
+                    for h in range(kv * (H // HK), (kv + 1) * (H // HK)):
+                        t.view(n, H, 128)[torch.tensor(rows).cuda(), h, cols] = y
+        else:
+            bad, clean, rows, kvs, cols = spoil(qkv, cu_h, spot)
+        vis = sees(cu_h, window)
+        q, k, v = qkv_views(bad, H, HK)
+        o, lse = torch.empty(n, H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, n, device="cuda")
+        gb.gptb_packed_attention(q, k, v, cu, o, lse, H, HK, window)
+        dqkv = torch.full_like(bad, 7.0)
+        ws = torch.full((gb.gptb_packed_attention_workspace_bytes(n, H),), 255, dtype=torch.uint8, device="cuda")
+        gb.gptb_packed_attention_backward(q, k, v, o, d_bad, lse, cu, *qkv_views(dqkv, H, HK), H, HK, window, ws)
+        assert gb.gptb_device_error() == 0
+        want = orl.packed_attention(*(heads(t[:m], h) for t, h in zip(qkv_views(clean, H, HK), (H, HK, HK))), cu_h, window,
+                                    heads(d_clean[:m], H))
+        bad_q = np.zeros((m, H), bool)
+        for kv in kvs:
+            own = name in ("q", "d")
+            bad_q[rows if own else vis[:, rows].any(1), kv * (H // HK):(kv + 1) * (H // HK)] = True
+        bad_kv = np.stack([vis[bad_q[:, kv * (H // HK):(kv + 1) * (H // HK)].any(1)].any(0) for kv in range(HK)], 1)
+        for what, t, hit in zip(("dq", "dk", "dv"), qkv_views(dqkv, H, HK), (bad_q, bad_kv, bad_kv)):
+            got = heads(t[:m], hit.shape[1])
+            within(np.where(hit[:, :, None], want[what], got), want[what], want["err"][what])
+            if np.isnan(x) and name in ("qkv", "q", "d"):
+                assert not np.isfinite(got[hit]).any()
+            assert torch.all(t[m:] == 7.0)
