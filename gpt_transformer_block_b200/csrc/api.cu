@@ -1702,6 +1702,12 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
   a.T_max = T_max;
   a.window = window;
   a.spt = prefix_spt(B, G);
+  a.q = static_cast<const bf16*>(q);
+  a.k_prefix = static_cast<const bf16*>(k_prefix);
+  a.v_prefix = static_cast<const bf16*>(v_prefix);
+  a.k_cache = static_cast<const bf16*>(k_cache);
+  a.v_cache = static_cast<const bf16*>(v_cache);
+  a.ld_prefix = ld_prefix;
   const PrefixWs w = prefix_ws(B, H, Hkv);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   a.plan = reinterpret_cast<int4*>(ws + w.plan);

@@ -78,6 +78,8 @@ struct PrefixArgs {
   const int32_t *cu_prefix, *cu_group, *lens;
   int total_prefix, n_groups, B, H, Hkv, T_max, window;
   int spt;       // sequences per query tile of a prefix segment (128 / G)
+  const bf16 *q, *k_prefix, *v_prefix, *k_cache, *v_cache;
+  long long ld_prefix;
   int4* plan;    // [B + 1]: first cost unit of the sequence's segments, prefix tiles, own tiles (-1: bad length),
                  // first sequence of its query tile; [B].x = all units
   float* rec_a;  // [2 sources][B*H][2][PD_REC] the share of a segment that starts it
@@ -604,11 +606,42 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   }
 }
 
+// o of (b, h) by one CTA from the keys that the window leaves it, in `part` as
+// one sum per warp: sum of exp2(s - m) inv v, s in base 2, 4 columns per lane.
+__device__ __noinline__ void prefix_alone(const PrefixArgs& a, int b, int h, float m, float inv, float (*part)[128]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = lane * 4, kvh = h / (a.H / a.Hkv);
+  const PdSeq s = pd_seq(a, b);
+  const int oldest = a.window < 0 ? 0 : (int)max(0ll, (long long)s.plen + s.len - 1 - a.window);  // position
+  const auto load4 = [&](const bf16* p, float (&x)[4]) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p + c);
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xffff0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xffff0000u);
+  };
+  float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+  load4(a.q + ((long long)b * a.H + h) * 128, qv);
+#pragma unroll 2
+  for (int pos = oldest + warp; pos < s.plen + s.len; pos += 4) {
+    const bool own = pos >= s.plen;
+    const long long row = own ? (long long)b * a.T_max + pos - s.plen : (long long)s.p0 + pos;
+    const long long at = row * (own ? (long long)a.Hkv * 128 : a.ld_prefix) + kvh * 128;
+    float k[4], v[4];
+    load4((own ? a.k_cache : a.k_prefix) + at, k);
+    load4((own ? a.v_cache : a.v_prefix) + at, v);
+    const float sc = warp_sum(fmaf(qv[0], k[0], fmaf(qv[1], k[1], fmaf(qv[2], k[2], qv[3] * k[3]))));
+    const float p = fast_exp2(fmaf(sc, LOG2E / sqrtf(128.f), -m)) * inv;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = fmaf(p, v[i], acc[i]);
+  }
+  *reinterpret_cast<float4*>(&part[warp][c]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+}
+
 // One CTA per (sequence, head) joins its partial results, its four warps a
 // quarter of them each: lane i takes the max and sum of the i-th one, then all
 // lanes add up 4 columns each.
 __global__ void __launch_bounds__(128)
-    prefix_combine_kernel(const PrefixArgs a, bf16* __restrict__ o, float* __restrict__ lse, int nctas) {
+    prefix_combine_kernel(const __grid_constant__ PrefixArgs a, bf16* __restrict__ o, float* __restrict__ lse, int nctas) {
   __shared__ float s_acc[4][128], s_m[4], s_l[4];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long bh = blockIdx.x;
@@ -692,7 +725,16 @@ __global__ void __launch_bounds__(128)
       x = fmaf(w, s_acc[q][threadIdx.x], x);
     }
   }
-  o[bh * 128 + threadIdx.x] = __float2bfloat16_rn(sum == 0.f ? 0.f : x / sum);
+  float y = sum == 0.f ? 0.f : x / sum;
+  // With a window the samples of a prompt see different rows of it, and a NaN or
+  // infinity of V that this one does not see has met its P = 0 all the same.  (V
+  // as large as 2^-8 of the type's largest may overflow before it is divided.)
+  if (finite(sum) && __syncthreads_or(!finite(y))) {
+    prefix_alone(a, b, h, mm, 1.f / sum, s_acc);
+    __syncthreads();
+    if (!finite(y)) y = (s_acc[0][threadIdx.x] + s_acc[1][threadIdx.x]) + (s_acc[2][threadIdx.x] + s_acc[3][threadIdx.x]);
+  }
+  o[bh * 128 + threadIdx.x] = __float2bfloat16_rn(y);
   if (threadIdx.x == 0 && lse) lse[bh] = sum == 0.f ? -INFINITY : (mm + log2f(sum)) * LN2;
 }
 

@@ -436,8 +436,8 @@ int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, 
  *   o:       device bf16 [B, H, 128]; lse: device fp32 [B, H] or NULL
  *   workspace: device, gptb_prefix_decode_workspace_bytes(B, H, Hkv) bytes,
  *            16-byte aligned; concurrent calls need one each
- * Cache rows from lens[b] on and prefix rows of other groups reach no result,
- * whatever they hold.  Results do not vary from run to run.
+ * Cache rows from lens[b] on, prefix rows of other groups and rows outside a
+ * sequence's window do not reach its result, whatever they hold.  Results do not vary from run to run.
  * Errors as for gptb_packed_attention; GPTB_ERR_WORKSPACE (too small),
  * GPTB_ERR_UNSUPPORTED (more than 128 query heads per kv head; more than 2^30
  * prefix or cache rows; B*Hkv times the 128-row tiles of T_max and total_prefix
