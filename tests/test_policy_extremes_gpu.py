@@ -102,3 +102,30 @@ def test_reference_without_its_term(cuda_lib, dtype, z_a):
     assert bool(torch.isfinite(dz).all()) and torch.equal(dz, dz0) and torch.equal(logp, logp0)
     assert bool(torch.isfinite(stats[0])) and stats[0] == stats0[0] and stats[2] == stats0[2]
     assert stats[1] == float("inf") and stats0[1] == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("V", [333, 4099, 50257])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (30, 5), (11, 8)])
+def test_where_the_gradient_goes_changes_no_result(cuda_lib, dtype, V, pad, offset):
+    """No gradient, one in an array of its own, in rows that lie otherwise, over the logits: the same bits (vectors are
+    cut at the logits' alignment, whatever the gradient's is)."""
+    gb = cuda_lib
+    d = policy_case(7, V, dtype, seed=26, pad=pad, offset=offset)
+    n = d["z"].shape[0]
+
+    def call(dz):
+        logp, stats = torch.full((n,), 7.0, device="cuda"), torch.full((3,), 7.0, device="cuda")
+        ws = torch.empty(gb.gptb_policy_loss_workspace_bytes(n), dtype=torch.uint8, device="cuda")
+        gb.gptb_policy_loss(d["z"], d["a"], d["w"], d["A"], d["old"], d["ref"], 0.2, 0.3, 0.1, dz, logp, stats, ws)
+        return logp, stats
+
+    want = call(None)
+    grads = [torch.full((n, V), 7.0, dtype=dtype, device="cuda"),
+             torch.full((n, V + 9), 7.0, dtype=dtype, device="cuda")[:, 3:V + 3],
+             torch.full((n, V + 8), 7.0, dtype=dtype, device="cuda")[:, 7:V + 7], d["z"]]
+    for dz in grads:  # (the last call overwrites the logits)
+        for x, y in zip(call(dz), want):
+            assert torch.equal(x, y)
+    for dz in grads[1:]:
+        assert torch.equal(dz, grads[0])
