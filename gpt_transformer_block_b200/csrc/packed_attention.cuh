@@ -70,13 +70,18 @@ __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // The rows of `again` (a bit per lane; the lane has row row0 + lane's first
 // visible key, maximum and inverse sum) once more, by the warp from the rows
-// that they see: o = sum of exp2(s - m) inv v, s in base 2, 4 columns per lane,
-// in the columns that are not finite at `at` (row 0, `pitch` bytes from row to
-// row; or, pitch 0, the swizzled tile).  From the newest key back, until all of
-// those columns are not finite again: nothing makes them so any more.
-__device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_lo, float m_used, float inv_l,
-                                               const bf16* q, long long ldq, const bf16* k, long long ldk, const bf16* v,
-                                               long long ldv, uint8_t* at0, long long pitch) {
+// that they see: o = sum of exp2(s - m) inv v, s in base 2, 4 columns per lane.
+// In the columns that are not finite at `at` (row 0, `pitch` bytes from row to
+// row; or, pitch 0, the swizzled tile), and for a row that sees many keys only in
+// those in which a V row is not finite that its tiles hold (v_first .. v_last)
+// and it does not see: else one NaN early in a long sequence would send all the
+// rows that do see it through here (8192 rows of 12 heads: 49 ms).  From the
+// newest key back, until none of those columns is finite any more: nothing makes
+// them so again.
+constexpr int PF_ALONE = 1024;  // keys
+__device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_lo, float m_used, float inv_l, int v_first,
+                                               int v_last, const bf16* q, long long ldq, const bf16* k, long long ldk,
+                                               const bf16* v, long long ldv, uint8_t* at0, long long pitch) {
   const int lane = threadIdx.x & 31, c = lane * 4;
   const auto four = [](const uint2& u, float (&x)[4]) {
     x[0] = __uint_as_float(u.x << 16);
@@ -93,11 +98,24 @@ __device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_
     uint2* at = reinterpret_cast<uint2*>(
         pitch ? at0 + x * pitch + lane * 8
               : at0 + (lane >> 4) * 16384 + x * 128 + ((((lane & 15) >> 1) ^ (x & 7)) << 4) + (lane & 1) * 8);
-    float old[4], a[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+    float old[4], a[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, foreign[4] = {0.f, 0.f, 0.f, 0.f};
     four(*at, old);
-    bool open = false;
+    const int before = max(0, lo - v_first), unseen = before + v_last - t;
+    if (t - lo < max(unseen, PF_ALONE)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) open |= !finite(old[i]);
+      for (int i = 0; i < 4; ++i) foreign[i] = INFINITY;
+    } else {  // (0 * x is NaN where x is not finite)
+#pragma unroll 4
+      for (int i = 0; i < unseen; ++i) {
+        float y[4];
+        load4(v + (long long)(i < before ? v_first + i : t + 1 + i - before) * ldv, y);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) foreign[e] = fmaf(0.f, y[e], foreign[e]);
+      }
+    }
+    bool want[4], open = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) open |= want[i] = !finite(old[i]) && foreign[i] != 0.f;
     load4(q + t * ldq, a);
 #pragma unroll 1
     for (int j0 = t; j0 >= lo && __any_sync(0xffffffffu, open); j0 -= 4) {
@@ -120,10 +138,10 @@ __device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_
       }
       open = false;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) open |= !finite(old[i]) && finite(acc[i]);
+      for (int i = 0; i < 4; ++i) open |= want[i] && finite(acc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) old[i] = finite(old[i]) ? old[i] : acc[i];
+    for (int i = 0; i < 4; ++i) old[i] = want[i] ? acc[i] : old[i];
     *at = make_uint2(pack_bf16(old[0], old[1]), pack_bf16(old[2], old[3]));
   }
 }
@@ -419,15 +437,15 @@ __global__ void __launch_bounds__(PF_THREADS, 2)
             *reinterpret_cast<uint4*>(o + (long long)tq * ldo + h * 128 + k * 32 + g * 8) = u;
         }
       }
-      // A row whose o is not finite may owe that to rows it does not see (P = 0
-      // there, and 0 * NaN is NaN), so it is worked out again from those that it
-      // sees
+      // A row whose o is not finite, though its sum is, may owe that to rows it
+      // does not see (P = 0 there, and 0 * NaN is NaN), so it is worked out again
+      // from those that it sees
       float a0, a1;
       f2_unpack(all, a0, a1);
       __syncwarp();
-      const unsigned again = __ballot_sync(0xffffffffu, tq < n_rows && !finite(a0 + a1));
+      const unsigned again = __ballot_sync(0xffffffffu, tq < n_rows && l > 0.f && finite(l) && !finite(a0 + a1));
       if (again)
-        packed_rows_alone(again, row0, kv_lo, m_used, inv, in.q + h * 128, in.ldq, in.k + kvh * 128, in.ldk, in.v + kvh * 128,
+        packed_rows_alone(again, row0, kv_lo, m_used, inv, n > PF_LONG ? lo : jlo * PF_BN, min(q0 + FA_BM, n_rows) - 1, in.q + h * 128, in.ldq, in.k + kvh * 128, in.ldk, in.v + kvh * 128,
                           in.ldv, whole ? sQ + qw * 4096 : reinterpret_cast<uint8_t*>(o + row0 * ldo + h * 128),
                           whole ? 0 : ldo * 2);
       fence_proxy_async_smem();

@@ -165,3 +165,27 @@ def test_backward(cuda_lib, batch, window, spot):
             if np.isnan(x) and name in ("qkv", "q", "d"):
                 assert not np.isfinite(got[hit]).any()
             assert torch.all(t[m:] == 7.0)
+
+
+@pytest.mark.parametrize("rows", [[1500], [3000, 3100], list(range(1200, 4000, 300))])
+@pytest.mark.parametrize("window", [-1, 1900])
+def test_rows_far_behind_a_spoilt_one(cuda_lib, rows, window):
+    """V rows of one kv head spoilt in the midst of long sequences: rows before them and of other sequences, also those
+    that share tiles with them, are not reached, rows that see one are."""
+    gb = cuda_lib
+    lens = [1900, 2300, 40]
+    qkv, _, cu = packed(lens, H, HK, seed=6)
+    q, k, v = qkv_views(qkv, H, HK)
+    cu_h = cu.cpu().numpy()
+    want = orl.packed_attention(*(heads(t, h) for t, h in zip((q, k, v), (H, HK, HK))), cu_h, window)
+    for r in rows:
+        v[r, 128:] = float("nan")
+    o, lse = torch.empty(len(qkv), H * 128, dtype=torch.bfloat16, device="cuda"), torch.empty(H, len(qkv), device="cuda")
+    gb.gptb_packed_attention(q, k, v, cu, o, lse, H, HK, window)
+    assert gb.gptb_device_error() == 0
+    hit = np.zeros((len(qkv), H), bool)
+    hit[:, 2:] = sees(cu_h, window)[:, rows].any(1)[:, None]
+    got = heads(o, H)
+    assert not np.isfinite(got[hit]).any()
+    within(np.where(hit[:, :, None], want["o"], got), want["o"], want["err"]["o"])
+    assert np.abs(lse.double().cpu().numpy() - want["lse"]).max() <= 1e-4
