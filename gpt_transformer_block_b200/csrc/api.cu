@@ -1761,7 +1761,7 @@ int policy_rows(const T* z, T* dz, PolicyArgs a, int* parts, cudaStream_t st) {
   // against 249 with one that takes the rest from L2, and 255 and 291 with three
   // and four, which hold all but wait for one another); more when there are
   // fewer rows than CTAs, down to two vectors per thread (29 bf16 rows of
-  // 32768: 8.8 us with 8, 9.7 with one)
+  // 32768: 10.3 us with 5, 12.3 with one)
   const long long row = ((long long)a.V * sizeof(T) + 15) / 16, ctas = std::max(1, dev_info().sms) * POL_CTAS;
   const long long hold = row > POL_KEEP * POL_THREADS ? 2 : 1;
   const long long fill = std::min(ctas / a.rows, row / (2 * POL_THREADS));

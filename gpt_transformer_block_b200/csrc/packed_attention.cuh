@@ -19,10 +19,10 @@
 // does not show itself in time, so in the forward a row whose result is not
 // finite is worked out again from the rows that it sees.
 //
-// The tile schedules are those of attention_tc.cuh: forward 256 queries of one
-// head per CTA over 128-key tiles, backward 128 keys of one kv head per CTA
-// over 64-query tiles; D, and the zeroing of the fp32 dQ sums, in a pass of
-// its own before, the rounding of dQ to bf16 in one after.
+// Forward: 128 queries of one head per CTA over 64-key tiles, two CTAs per SM.
+// Backward: the schedule of attention_tc.cuh, 128 keys of one kv head per CTA
+// over 64-query tiles; D, and the zeroing of the fp32 dQ sums, in a pass of its
+// own before, the rounding of dQ to bf16 in one after.
 #pragma once
 #include "attention_tc.cuh"
 #include "common.cuh"
@@ -157,10 +157,12 @@ __device__ __noinline__ void packed_rows_alone(unsigned again, int row0, int kv_
 // bf16, and the normalisation uses the same maximum, so the result is exact).
 // What bounds it: the softmax (its exponentials alone take half of the time on
 // their unit), and the start and end of a CTA, which the other CTA of the SM
-// fills.  One sequence of 8192 rows, 12 heads: 205 us, 24 ragged
-// ones (1 to 2000 rows, 10 heads, window 1024): 65 us; with 128-key tiles and so
-// no room for a second S 204 and 73, as one CTA of two query tiles per SM
-// (attention_tc.cuh) 220 and 84.
+// fills.  One sequence of 8192 rows, 12 heads: 205 us, 24 ragged ones (30 to 2000
+// rows, 10 heads, window 1024): 65 us.  With 128-key tiles, and so no room for a
+// second S, 204 and 73: the long sequence gains nothing by it, the ragged ones
+// do.  As one CTA of two query tiles per SM (attention_tc.cuh) 220 and 84.  (All
+// on one GPU; the long sequence takes up to 235 us on others, or where the power
+// cap holds the clock lower.)
 constexpr int PF_THREADS = 192;
 constexpr int PF_BN = 64;
 constexpr int PF_LONG = 32;                                // key tiles, 2048 keys
@@ -950,8 +952,8 @@ __global__ void __launch_bounds__(AB2_THREADS, 1)
 // 1 / sqrt(visible keys).  So for rows that see at most PB_FEW keys D is taken
 // as the sum of P dP, which needs no o: two lanes per key, by CTAs of their own.  (Without it dq and
 // dk of 5 sequences of 12 to 180 tokens were 2.6e-3 off in the norm, with it
-// 2.4e-3; 1.7e-3 is the rounding of the result alone.  14600 rows of 12 heads: 44
-// us, 33 without the rows of few keys.)
+// 2.4e-3; 1.7e-3 is the rounding of the result alone.  15733 rows of 12 heads: 44
+// us; forward and backward together take 5 us less without the rows of few keys.)
 constexpr int PB_FEW = 16;
 constexpr int PB_PRE_ROWS = 16;  // most rows of a CTA
 
@@ -1052,7 +1054,7 @@ __global__ void __launch_bounds__(256)
 }
 
 // After it: dQ rounded to bf16, 8 columns per thread; bound by HBM (6 bytes per
-// element: 14600 rows of 12 heads in 20 us, 6.7 TB/s, some of it still in L2).
+// element: 15733 rows of 12 heads in 20 us, 7.2 TB/s, some of it still in L2).
 __global__ void __launch_bounds__(256)
     packed_attn_dq_kernel(const float* __restrict__ acc, bf16* __restrict__ dq, long long lddq,
                           const int32_t* __restrict__ cu, int n_seq, int total, int H) {

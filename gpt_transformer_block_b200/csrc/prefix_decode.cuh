@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
                         const PrefixArgs a) {
   extern __shared__ uint8_t pd_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(pd_smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                  // one or two segments' query rows
+  uint8_t* sQ = smem;                  // the query rows of up to PD_QS segments
   uint8_t* sK = sQ + PD_TILE;          // PD_ST stages
   uint8_t* sV = sK + PD_ST * PD_TILE;  // PD_ST stages
   __shared__ __align__(8) uint64_t bars[9 + 4 * PD_ST + 2 * PD_QS];

@@ -387,6 +387,9 @@ int gptb_decode_attention(const void* q, const void* k_cache, const void* v_cach
  * result, and their outputs are left as they were.  A NaN or infinity in a row
  * of k or v reaches o (and one of k lse) of the rows that see it, one of q that
  * of its own row, and nothing else.  Outputs overlap no input.
+ * Scores and lse are fp32: q k / sqrt(128) up to 2^26 in magnitude (lse is off
+ * by 2^-24 of it, the backward's probabilities by as much, relative), v up to
+ * 2^100.
  * Offsets that break the order above are reported by gptb_device_error()
  * (GPTB_ERR_BAD_INPUT); the outputs are then undefined, and nothing outside
  * the arrays is touched.
@@ -405,7 +408,8 @@ int gptb_packed_attention(const void* q, long long ldq, const void* k, long long
  *   workspace: device, gptb_packed_attention_workspace_bytes(total, H) bytes,
  *            16-byte aligned
  * dq is summed over key tiles by fp32 reductions whose order varies, so its
- * last bit may differ from run to run; dk and dv do not vary. */
+ * last bit may differ from run to run; dk and dv do not vary.  Calls that may run
+ * at the same time (two captured graphs, say) need a workspace each. */
 size_t gptb_packed_attention_workspace_bytes(int total, int H);
 int gptb_packed_attention_backward(const void* q, long long ldq, const void* k, long long ldk, const void* v,
                                    long long ldv, const void* o, long long ldo, const void* dout, long long lddo,
@@ -457,7 +461,8 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
  * and dlogits = d loss / d logits (a clipped row keeps its KL term only).
  *   logits:  device, `rows` rows of `vocab` elements (GPTB_BF16 or GPTB_F32),
  *            ld elements from row to row; any alignment of an element (16-byte
- *            aligned rows are the fastest)
+ *            aligned rows are the fastest); any finite values, and -inf for
+ *            tokens that are ruled out (probability and gradient 0)
  *   actions: device int32 [rows]; one outside [0, vocab) is reported by
  *            gptb_device_error() (GPTB_ERR_BAD_INPUT), its row counts as
  *            weight 0
@@ -473,7 +478,7 @@ int gptb_prefix_decode_attention(const void* q, const void* k_prefix, const void
  *            With beta = 0 and a logp_ref the second is computed all the same
  *            and reaches neither the loss nor the gradient
  *   workspace: device, gptb_policy_loss_workspace_bytes(rows) bytes, 16-byte
- *            aligned
+ *            aligned; concurrent calls need one each
  * logits, dlogits and the per-row arrays need their elements' alignment only.
  * Results do not vary from run to run.  Errors: GPTB_ERR_INVALID_ARG (shapes, strides, clip borders, beta; more
  * than 2^29 rows), GPTB_ERR_UNSUPPORTED (dtype), GPTB_ERR_WORKSPACE. */
